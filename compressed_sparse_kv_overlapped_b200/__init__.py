@@ -27,11 +27,17 @@ CSA_OP_SPARSE_ATTN = 2
 CSA_OP_HCA_ATTN = 3
 CSA_OP_DECODE = 4
 CSA_OP_PREFILL = 5
+CSA_OP_WINDOW_ATTN = 6
+CSA_OP_PREFIX_ATTN = 7
+
+CSA_KV_BF16 = 0
+CSA_KV_F16 = 1
 
 EXPORTS = ("csa_compress", "csa_compress_all", "csa_index_topk", "csa_sparse_attn", "hca_dense_attn", "hybrid_attn_decode",
            "hybrid_attn_prefill", "csa_workspace_size", "csa_last_error", "csa_sync_status", "csa_version",
            "csa_set_stage_events", "csa_index_topk_noalloc", "csa_debug_inject", "csa_quantize_keys",
-           "csa_index_topk_mx8", "csa_quantize_entries", "csa_sparse_attn_fp4", "hca_dense_attn_fp4")
+           "csa_index_topk_mx8", "csa_quantize_entries", "csa_sparse_attn_fp4", "hca_dense_attn_fp4",
+           "csa_kv_append", "csa_window_attn", "csa_prefix_attn")
 CSA_DECODE_MARKS = 5
 
 _i32, _i64, _f32, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
@@ -67,6 +73,24 @@ class csa_prefill_args(ctypes.Structure):
                 ("idx_key", _vp), ("bias_c", _vp), ("bias_h", _vp), ("entries", _vp), ("entry_keys", _vp),
                 ("hca_entries", _vp), ("q", _vp), ("q_idx", _vp), ("w", _vp), ("out", _vp), ("lse", _vp),
                 ("idx_out", _vp), ("idx_in", _vp), ("norms", ctypes.POINTER(csa_norms))]
+
+
+class csa_kv_cache(ctypes.Structure):
+    _fields_ = [("H", _i32), ("H_kv", _i32), ("d", _i32), ("type", _i32), ("page_size", _i32), ("B", _i32),
+                ("num_pages", _i64), ("max_pages", _i64), ("page_stride", _i64), ("slot_stride", _i64),
+                ("head_stride", _i64), ("k_pages", _vp), ("v_pages", _vp), ("page_table", _vp), ("seqs", _vp)]
+
+
+class csa_kv_append_args(ctypes.Structure):
+    _fields_ = [("kv", csa_kv_cache), ("rows", _i64), ("max_n", _i64), ("k", _vp), ("v", _vp), ("q", _vp),
+                ("q_out", _vp), ("k_stride", _i64), ("v_stride", _i64), ("q_stride", _i64), ("q_out_stride", _i64),
+                ("inv_freq", _vp), ("rot", _i32), ("interleaved", _i32)]
+
+
+class csa_kv_attn_args(ctypes.Structure):
+    _fields_ = [("kv", csa_kv_cache), ("rows", _i64), ("max_n", _i64), ("max_len", _i64), ("W", _i64), ("S", _i64),
+                ("prefix_len", _i64), ("scale", _f32), ("reserved", _i32), ("q", _vp), ("out", _vp), ("lse", _vp),
+                ("q_stride", _i64), ("out_stride", _i64)]
 
 
 _lib = None
@@ -108,10 +132,14 @@ def lib() -> ctypes.CDLL:
                                           _vp, _vp, _sz, _vp]
         L.hca_dense_attn_fp4.argtypes = [P(csa_dims), _vp, _vp, ctypes.c_int, _i64, _vp, _vp, _vp, _vp, ctypes.c_int,
                                          _f32, _vp, _vp, _vp, _sz, _vp]
+        L.csa_kv_append.argtypes = [P(csa_kv_append_args), _vp]
+        L.csa_window_attn.argtypes = [P(csa_kv_attn_args), _vp, _sz, _vp]
+        L.csa_prefix_attn.argtypes = [P(csa_kv_attn_args), _vp, _sz, _vp]
         for n in ("csa_compress", "csa_compress_all", "csa_index_topk", "csa_sparse_attn", "hca_dense_attn", "hybrid_attn_decode",
                   "hybrid_attn_prefill", "csa_sync_status", "csa_version", "csa_set_stage_events",
                   "csa_index_topk_noalloc", "csa_debug_inject", "csa_quantize_keys", "csa_index_topk_mx8",
-                  "csa_quantize_entries", "csa_sparse_attn_fp4", "hca_dense_attn_fp4"):
+                  "csa_quantize_entries", "csa_sparse_attn_fp4", "hca_dense_attn_fp4", "csa_kv_append",
+                  "csa_window_attn", "csa_prefix_attn"):
             getattr(L, n).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -286,8 +314,25 @@ def hybrid_attn_prefill(args: csa_prefill_args, ws, stream=None) -> None:
     _check(rc, "hybrid_attn_prefill")
 
 
+def csa_kv_append(args: csa_kv_append_args, stream=None) -> None:
+    _check(lib().csa_kv_append(ctypes.byref(args), _vp(_stream(stream))), "csa_kv_append")
+
+
+def csa_window_attn(args: csa_kv_attn_args, ws, stream=None) -> None:
+    rc = lib().csa_window_attn(ctypes.byref(args), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                               _vp(_stream(stream)))
+    _check(rc, "csa_window_attn")
+
+
+def csa_prefix_attn(args: csa_kv_attn_args, ws, stream=None) -> None:
+    rc = lib().csa_prefix_attn(ctypes.byref(args), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                               _vp(_stream(stream)))
+    _check(rc, "csa_prefix_attn")
+
+
 def build() -> str:
     return _build.build()
 
 
 from .layer import HybridLayer  # noqa: E402  (torch-side cache allocation; imports torch lazily)
+from .paged import PagedKV  # noqa: E402

@@ -772,6 +772,8 @@ size_t csa_workspace_size(int op, const void* args) {
         if (check_dims(&a->dims) || a->q_end < 1) return 0;
         return plan_prefill(a->dims, a->q_end).total;
     }
+    if (op == CSA_OP_WINDOW_ATTN || op == CSA_OP_PREFIX_ATTN)
+        return paged_workspace_size(static_cast<const csa_kv_attn_args*>(args), op);
     return 0;
 }
 

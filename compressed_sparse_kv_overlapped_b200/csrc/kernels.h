@@ -281,6 +281,9 @@ int device_status(int** out);
 // next attention launches use.
 void debug_fault_state(int* fault, uint64_t* wait_ns);
 
+// Workspace of csa_window_attn / csa_prefix_attn (paged.cu); 0 for invalid arguments.
+size_t paged_workspace_size(const csa_kv_attn_args* args, int op);
+
 // Error reporting shared by entry points defined outside capi.cu.
 int validate_dims(const csa_dims* d);             // CSA_OK or the error code (message set)
 int set_error(int code, const char* fmt, ...);    // records the message for csa_last_error()

@@ -1,0 +1,237 @@
+// paged.cu -- C entry points of the paged key/value operators (declared in include/csa.h): host-side
+// checks, the split of long rows, workspace layout and launches.
+#include <cmath>
+
+#include "kernels.h"
+#include "paged.h"
+
+namespace csa {
+
+namespace {
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // token positions and counts fit 32 bits on the device
+constexpr size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool stride_ok(int64_t v, int64_t least) { return v >= least && v % 8 == 0 && v < (int64_t)1 << 36; }
+
+// Checks of the cache's shape (`pointers`: and of its pointers).
+int check_cache(const csa_kv_cache& kv, bool pointers) {
+    if (kv.d != 64 && kv.d != 128) return set_error(CSA_ERR_UNSUPPORTED, "d = %d (supported: 64, 128)", kv.d);
+    if (kv.type != CSA_KV_BF16 && kv.type != CSA_KV_F16)
+        return set_error(CSA_ERR_UNSUPPORTED, "type = %d (CSA_KV_BF16 or CSA_KV_F16)", kv.type);
+    if (kv.H < 1 || kv.H > 256) return set_error(CSA_ERR_UNSUPPORTED, "H = %d (supported: 1..256)", kv.H);
+    if (kv.H_kv < 1 || kv.H % kv.H_kv) return set_error(CSA_ERR_ARG, "H_kv = %d does not divide H = %d", kv.H_kv, kv.H);
+    if (kv.H / kv.H_kv > 64)
+        return set_error(CSA_ERR_UNSUPPORTED, "%d query heads on a key head (supported: 1..64)", kv.H / kv.H_kv);
+    if (kv.page_size < 16 || kv.page_size > 256 || (kv.page_size & (kv.page_size - 1)))
+        return set_error(CSA_ERR_UNSUPPORTED, "page_size = %d (supported: powers of two from 16 to 256)", kv.page_size);
+    if (kv.B < 1 || kv.num_pages < 1 || kv.max_pages < 1)
+        return set_error(CSA_ERR_ARG, "B = %d, num_pages = %lld, max_pages = %lld", kv.B, (long long)kv.num_pages,
+                         (long long)kv.max_pages);
+    if (kv.max_pages > kMaxTokens / kv.page_size || kv.num_pages > 0x7fffffff)
+        return set_error(CSA_ERR_UNSUPPORTED, "max_pages = %lld of %d tokens, num_pages = %lld", (long long)kv.max_pages,
+                         kv.page_size, (long long)kv.num_pages);
+    if (!stride_ok(kv.page_stride, kv.num_pages > 1 ? 8 : 0) || !stride_ok(kv.slot_stride, 8) ||
+        !stride_ok(kv.head_stride, kv.H_kv > 1 ? 8 : 0))
+        return set_error(CSA_ERR_ARG, "page_stride = %lld, slot_stride = %lld, head_stride = %lld (multiples of 8)",
+                         (long long)kv.page_stride, (long long)kv.slot_stride, (long long)kv.head_stride);
+    if (!pointers) return CSA_OK;
+    if (!kv.k_pages || !kv.v_pages || !kv.page_table || !kv.seqs) return set_error(CSA_ERR_ARG, "NULL pointer argument");
+    if (!aligned16(kv.k_pages) || !aligned16(kv.v_pages))
+        return set_error(CSA_ERR_ARG, "pages must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(kv.page_table) & 3u) || (reinterpret_cast<uintptr_t>(kv.seqs) & 7u))
+        return set_error(CSA_ERR_ARG, "page_table must be 4-byte, seqs 8-byte aligned");
+    return CSA_OK;
+}
+
+int check_rows(int64_t rows, int64_t max_n) {
+    if (rows < 0 || rows >= kMaxTokens || max_n < 0)
+        return set_error(CSA_ERR_ARG, "rows = %lld, max_n = %lld", (long long)rows, (long long)max_n);
+    return CSA_OK;
+}
+
+// Shape checks of an attention call; op: CSA_OP_WINDOW_ATTN or CSA_OP_PREFIX_ATTN.
+int check_attn(const csa_kv_attn_args& a, int op) {
+    int rc = check_cache(a.kv, false);
+    if (rc) return rc;
+    if ((rc = check_rows(a.rows, a.max_n))) return rc;
+    if (a.max_len < 0) return set_error(CSA_ERR_ARG, "max_len = %lld", (long long)a.max_len);
+    if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return set_error(CSA_ERR_ARG, "scale = %g", (double)a.scale);
+    if (a.reserved != 0) return set_error(CSA_ERR_ARG, "reserved must be 0");
+    if (op == CSA_OP_WINDOW_ATTN) {
+        if (a.W < 1 || a.S < 0 || a.prefix_len != 0)
+            return set_error(CSA_ERR_ARG, "W = %lld (>= 1), S = %lld (>= 0), prefix_len = %lld (0)", (long long)a.W,
+                             (long long)a.S, (long long)a.prefix_len);
+    } else {
+        if (a.W != 0 || a.S != 0 || a.prefix_len < 0)
+            return set_error(CSA_ERR_ARG, "W = %lld (0), S = %lld (0), prefix_len = %lld (>= 0)", (long long)a.W,
+                             (long long)a.S, (long long)a.prefix_len);
+        if (a.prefix_len > a.kv.max_pages * a.kv.page_size)
+            return set_error(CSA_ERR_ARG, "prefix_len = %lld exceeds a row of the page table", (long long)a.prefix_len);
+    }
+    return CSA_OK;
+}
+
+// How a call is cut: the partial slots of its launches (1 launch without a split needs none).
+struct PagedPlan {
+    int splits_window;  // window / suffix launch
+    int splits_prefix;  // prefix launch (0: none)
+    int slots;          // partials per (row, head); 0: written directly
+    size_t off_lse, total;
+};
+
+int sm_count_or(int dflt) {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();  // no device here: the plan of a full-size part
+        return dflt;
+    }
+    return n;
+}
+
+// Splits of a launch of `items` blocks over up to `keys` keys each.
+int plan_splits(int64_t items, int64_t keys, int sms) {
+    const int64_t by_keys = keys / 256 > 1 ? keys / 256 : 1;
+    const int64_t by_sms = items > 0 && sms / items > 1 ? sms / items : 1;
+    const int64_t s = by_keys < by_sms ? by_keys : by_sms;
+    return (int)(s < 256 ? s : 256);
+}
+
+PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
+    PagedPlan pl{};
+    const int64_t G = a.kv.H / a.kv.H_kv, cap = a.kv.max_pages * a.kv.page_size;
+    const int64_t max_len = a.max_len < cap ? a.max_len : cap, n = a.max_n < max_len ? a.max_n : max_len;
+    const int sms = sm_count_or(148);
+    auto row_tiles = [&](int64_t rows) { return (rows * G + 31) / 32; };
+    if (op == CSA_OP_WINDOW_ATTN) {
+        const int64_t win = a.W < max_len ? a.W + n - 1 + (a.S < max_len ? a.S : max_len) : max_len;
+        pl.splits_window = plan_splits(a.kv.B * a.kv.H_kv * row_tiles(n), win < max_len ? win : max_len, sms);
+        pl.slots = pl.splits_window > 1 ? pl.splits_window : 0;
+    } else {
+        const int64_t suffix = max_len > a.prefix_len ? max_len - a.prefix_len : 0;
+        pl.splits_window = plan_splits(a.kv.B * a.kv.H_kv * row_tiles(n), suffix, sms);
+        if (a.prefix_len > 0) pl.splits_prefix = plan_splits(a.kv.H_kv * row_tiles(a.rows), a.prefix_len, sms);
+        pl.slots = pl.splits_window + pl.splits_prefix;
+        if (pl.slots == 1) pl.slots = 0;
+    }
+    const size_t heads = (size_t)a.rows * a.kv.H * pl.slots;
+    pl.off_lse = align256(heads * a.kv.d * 4);
+    pl.total = pl.off_lse + align256(heads * 4);
+    if (pl.total < 256) pl.total = 256;
+    return pl;
+}
+
+int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!a) return set_error(CSA_ERR_ARG, "args is NULL");
+    int rc = check_attn(*a, op);
+    if (rc) return rc;
+    if (a->rows == 0 || a->max_n == 0 || a->max_len == 0) return CSA_OK;  // no query anywhere
+    if ((rc = check_cache(a->kv, true))) return rc;
+    if (!a->q || !a->out) return set_error(CSA_ERR_ARG, "NULL pointer argument");
+    if (!aligned16(a->q) || !aligned16(a->out) || (reinterpret_cast<uintptr_t>(a->lse) & 3u))
+        return set_error(CSA_ERR_ARG, "q and out must be 16-byte, lse 4-byte aligned");
+    const int64_t width = (int64_t)a->kv.H * a->kv.d;
+    if (!stride_ok(a->q_stride, width) || !stride_ok(a->out_stride, width))
+        return set_error(CSA_ERR_ARG, "q_stride = %lld, out_stride = %lld (multiples of 8, >= H d = %lld)",
+                         (long long)a->q_stride, (long long)a->out_stride, (long long)width);
+    const PagedPlan pl = make_plan(*a, op);
+    if (pl.slots && (!ws || ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(ws) & 255u)))
+        return set_error(CSA_ERR_ARG, "workspace: %zu bytes at a 256-byte aligned address needed, %zu given", pl.total,
+                         ws ? ws_bytes : (size_t)0);
+    PagedAttnParams p{};
+    p.kv = a->kv;
+    p.rows = a->rows;
+    p.max_n = (int)(a->max_n < a->rows ? a->max_n : a->rows);
+    p.prefix_len = (int)a->prefix_len;
+    p.key_begin = (int)a->prefix_len;
+    p.W = op == CSA_OP_WINDOW_ATTN && a->W < 0x7fffffff ? (int)a->W : 0x7fffffff;
+    p.S = (int)(a->S < kMaxTokens ? a->S : kMaxTokens);
+    p.scale_log2 = a->scale * 1.44269504088896340736f;
+    p.q = static_cast<const uint16_t*>(a->q);
+    p.out = static_cast<uint16_t*>(a->out);
+    p.lse = a->lse;
+    p.q_stride = a->q_stride;
+    p.out_stride = a->out_stride;
+    if (pl.slots) {
+        p.part_o = static_cast<float*>(ws);
+        p.part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + pl.off_lse);
+    }
+    if ((rc = device_status(&p.status))) return rc;
+    int fault = 0;
+    debug_fault_state(&fault, &p.wait_ns);
+    p.splits = pl.splits_window;
+    cudaError_t e = launch_paged_stream(p, stream);
+    if (e == cudaSuccess && pl.splits_prefix) {
+        PagedAttnParams f = p;
+        f.prefix_mode = 1;
+        f.key_begin = 0;
+        f.splits = pl.splits_prefix;
+        f.part_base = pl.splits_window;
+        e = launch_paged_stream(f, stream);
+    }
+    if (e == cudaSuccess && pl.slots) e = launch_paged_combine(p, pl.slots, stream, true);
+    if (e != cudaSuccess) return set_error(CSA_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
+    return CSA_OK;
+}
+
+}  // namespace
+
+size_t paged_workspace_size(const csa_kv_attn_args* a, int op) {
+    return check_attn(*a, op) ? 0 : make_plan(*a, op).total;
+}
+
+}  // namespace csa
+
+using namespace csa;
+
+extern "C" {
+
+int csa_kv_append(const csa_kv_append_args* a, csa_stream_t stream) {
+    if (!a) return set_error(CSA_ERR_ARG, "args is NULL");
+    int rc = check_cache(a->kv, false);
+    if (rc) return rc;
+    if ((rc = check_rows(a->rows, a->max_n))) return rc;
+    const csa_kv_cache& kv = a->kv;
+    if (a->rot < 0 || a->rot > kv.d || a->rot % 16)
+        return set_error(CSA_ERR_UNSUPPORTED, "rot = %d (supported: multiples of 16 from 0 to d)", a->rot);
+    if (a->interleaved != 0 && a->interleaved != 1) return set_error(CSA_ERR_ARG, "interleaved = %d", a->interleaved);
+    if (a->rows == 0 || a->max_n == 0) return CSA_OK;
+    if ((rc = check_cache(kv, true))) return rc;
+    if (!a->k || !a->v || (a->rot && !a->inv_freq)) return set_error(CSA_ERR_ARG, "NULL pointer argument");
+    if ((a->q == nullptr) != (a->q_out == nullptr)) return set_error(CSA_ERR_ARG, "q and q_out go together");
+    if (!aligned16(a->k) || !aligned16(a->v) || !aligned16(a->q) || !aligned16(a->q_out) ||
+        (reinterpret_cast<uintptr_t>(a->inv_freq) & 3u))
+        return set_error(CSA_ERR_ARG, "token arrays must be 16-byte, inv_freq 4-byte aligned");
+    const int64_t wk = (int64_t)kv.H_kv * kv.d, wq = (int64_t)kv.H * kv.d;
+    if (!stride_ok(a->k_stride, wk) || !stride_ok(a->v_stride, wk) ||
+        (a->q && (!stride_ok(a->q_stride, wq) || !stride_ok(a->q_out_stride, wq))))
+        return set_error(CSA_ERR_ARG, "row strides must be multiples of 8 and hold all heads");
+    PagedAppendParams p{};
+    p.kv = kv;
+    p.rows = a->rows;
+    p.max_n = a->max_n < a->rows ? a->max_n : a->rows;
+    p.k = static_cast<const uint16_t*>(a->k);
+    p.v = static_cast<const uint16_t*>(a->v);
+    p.q = static_cast<const uint16_t*>(a->q);
+    p.q_out = static_cast<uint16_t*>(a->q_out);
+    p.k_stride = a->k_stride;
+    p.v_stride = a->v_stride;
+    p.q_stride = a->q_stride;
+    p.q_out_stride = a->q_out_stride;
+    p.inv_freq = a->inv_freq;
+    p.rot = a->rot;
+    p.interleaved = a->interleaved;
+    if ((rc = device_status(&p.status))) return rc;
+    const cudaError_t e = launch_paged_append(p, stream);
+    return e == cudaSuccess ? CSA_OK : set_error(CSA_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
+}
+
+int csa_window_attn(const csa_kv_attn_args* args, void* ws, size_t ws_bytes, csa_stream_t stream) {
+    return run_attn(args, CSA_OP_WINDOW_ATTN, ws, ws_bytes, stream);
+}
+
+int csa_prefix_attn(const csa_kv_attn_args* args, void* ws, size_t ws_bytes, csa_stream_t stream) {
+    return run_attn(args, CSA_OP_PREFIX_ATTN, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,115 @@
+// paged.h -- the paged key/value operators (csa_kv_append, csa_window_attn, csa_prefix_attn): launch
+// interface between their C entry points (paged.cu) and kernels, and the device code both attention
+// kernels share: which keys a block of queries sees, and where they lie.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace csa {
+
+struct PagedAppendParams {
+    csa_kv_cache kv;
+    int64_t rows, max_n;
+    const uint16_t* k;
+    const uint16_t* v;
+    const uint16_t* q;  // nullable
+    uint16_t* q_out;
+    int64_t k_stride, v_stride, q_stride, q_out_stride;
+    const float* inv_freq;
+    int rot, interleaved;
+    int* status;
+};
+cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t stream);
+
+// One launch of an attention kernel over keys [key_begin, key_end of the mode) of every query.
+struct PagedAttnParams {
+    csa_kv_cache kv;
+    int64_t rows;
+    int max_n;
+    // the rows of a block of queries: 0 = one sequence's new tokens, each seeing its window and first
+    // tokens from key_begin on; 1 = all rows of the token arrays, each seeing the prefix
+    // [0, prefix_len) through row 0 of the table
+    int prefix_mode;
+    int prefix_len;     // sequences need len - n >= prefix_len (0: no prefix)
+    int key_begin;      // first key (the suffix of csa_prefix_attn: prefix_len)
+    int W, S;           // window (2^31 - 1: none) and first tokens
+    float scale_log2;   // scale * log2(e)
+    const uint16_t* q;
+    uint16_t* out;
+    float* lse;         // nullable
+    int64_t q_stride, out_stride;
+    // splits of the keys of a block: 1 with part_o = nullptr writes out / lse; otherwise split s of
+    // this launch writes the partial slot part_base + s: part_o [slot][rows][H][d] (normalized, fp32),
+    // part_lse [slot][rows][H] (base 2; -inf: an empty partial, its part_o is not written)
+    int splits, part_base;
+    float* part_o;
+    float* part_lse;
+    int* status;
+    uint64_t wait_ns;
+};
+
+// Few query rows per key (decode): mma.sync tiles of 16 or 32 rows, each warp streaming its own keys.
+cudaError_t launch_paged_stream(const PagedAttnParams& p, cudaStream_t stream, bool pdl = false);
+// Merge of `slots` partials per (row, head) into out / lse.
+cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots, cudaStream_t stream, bool pdl);
+
+// ---------------------------------------------------------------------------------------------
+
+// Sequence b of the table, checked; false: it is skipped (and reported by the thread with `say`).
+__device__ __forceinline__ bool paged_seq(const csa_kv_cache& kv, int b, int64_t rows, int64_t max_n, int prefix_len,
+                                          int* status, bool say, csa_kv_seq* out) {
+    const csa_kv_seq s = kv.seqs[b];
+    *out = s;
+    if (s.n == 0) return false;
+    const bool ok = s.n > 0 && s.n <= max_n && s.len >= s.n && s.len <= kv.max_pages * kv.page_size &&
+                    s.row >= 0 && s.n <= rows && s.row <= rows - s.n && s.len - s.n >= prefix_len;
+    if (!ok && say) report(status, CSA_ERR_INDEX);
+    return ok;
+}
+
+// The keys that a block of queries with positions [p0, p0 + cnt) sees, as two runs of tokens: the first
+// tokens [0, s1) and the window part [lo, hi), s1 <= lo.  Every query of the block sees all of the
+// first run; the second needs a mask per query.
+struct KeySpan {
+    int s1, lo, hi;
+};
+__device__ __forceinline__ KeySpan key_span(const PagedAttnParams& p, int64_t p0, int64_t cnt) {
+    KeySpan k;
+    if (p.prefix_mode) {
+        k.s1 = k.lo = 0;
+        k.hi = p.prefix_len;
+        return k;
+    }
+    const int64_t lo = p0 - (int64_t)p.W + 1;
+    k.lo = (int)(lo > p.key_begin ? lo : p.key_begin);
+    k.hi = (int)(p0 + cnt);
+    k.s1 = p.S < k.lo ? p.S : k.lo;
+    if (k.s1 < p.key_begin) k.s1 = 0;  // (key_begin > 0 only without first tokens)
+    return k;
+}
+
+// Bits [from, to) of a 16-key group that starts at token t0: the tokens of [a, b) in it.
+__device__ __forceinline__ uint32_t span16(int t0, int a, int b) {
+    int f = a - t0, e = b - t0;
+    f = f < 0 ? 0 : (f > 16 ? 16 : f);
+    e = e < 0 ? 0 : (e > 16 ? 16 : e);
+    return ((1u << e) - 1u) & ~((1u << f) - 1u);
+}
+
+// log2 of the page size (a power of two).
+__device__ __forceinline__ int page_shift(const csa_kv_cache& kv) { return 31 - __clz(kv.page_size); }
+
+// The page of token t through `table`, or -1 (reported) when its number is out of range.
+__device__ __forceinline__ int page_of(const csa_kv_cache& kv, const int32_t* table, int shift, int t, int* status) {
+    const int pg = __ldg(table + (t >> shift));
+    if (pg < 0 || pg >= kv.num_pages) {
+        report(status, CSA_ERR_INDEX);
+        return -1;
+    }
+    return pg;
+}
+
+}  // namespace csa

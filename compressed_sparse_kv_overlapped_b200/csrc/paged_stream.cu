@@ -1,0 +1,437 @@
+// paged_stream.cu -- attention of few query rows over a paged cache (decode steps, proposed tokens),
+// and the merge of partial results.
+//
+// With G = H / H_kv query heads per key head a decode step does 4 G d operations per 4 d bytes of key
+// and value, so the kernel is a read of the cache: what matters is bytes in flight and how little a
+// key costs on the way.  A block takes one (sequence, 16 or 32 query rows, key head) and a share of
+// its keys; rows are (token, head of the group) pairs.  Its eight warps are independent streams: warp
+// w takes the 16-key groups w, w + 8, ... of the block's share, copies them through a ring of its own
+// (cp.async, kStages groups ahead, no barrier among warps) and keeps its own running maximum, sum and
+// output, in the online softmax form
+//     m' = max(m, max_t x_t),  l' = l 2^(m - m') + sum_t 2^(x_t - m'),  o' = o 2^(m - m') + sum_t 2^(x_t - m') V_t
+// with x in base-2 units.  The eight results meet once, in shared memory at the end.
+//
+// A 16-key group never crosses a page (pages are multiples of 16 and groups are aligned to 16 tokens),
+// so it costs one page lookup, made one group ahead of its copies.  Keys outside the visible runs are
+// filled with zeros without being read: a freed page or an unwritten slot may hold anything, and a
+// weight of zero does not remove a NaN.  The two products run on mma.sync m16n8k16: the tensor pipe
+// is far from a limit here (32 of them per 8 KiB at d = 128) and tcgen05 would want 128 rows.
+#include <cfloat>
+
+#include "paged.h"
+
+namespace csa {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+
+template <int D, int MT>
+struct StreamCfg {
+    static constexpr int kRows = 16 * MT;
+    static constexpr int kGroup = 16 * D * 2;      // bytes of one group's keys (or values)
+    static constexpr int kStages = D == 128 ? 3 : 5;
+    static constexpr int kWarpBytes = kStages * 2 * kGroup;
+    static constexpr int kOStride = D + 4;         // floats; the padding spreads the rows over the banks
+    static constexpr int kOBytes = kRows * kOStride * 4;  // a warp's result, in its own ring
+    static_assert(kOBytes <= kWarpBytes, "the result fits the ring");
+    static constexpr int kML = kWarps * kWarpBytes;  // float2 [kWarps][kRows]: maximum and sum
+    static constexpr int kTotal = kML + kWarps * kRows * 8;
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if (F16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return pack_bf16x2(lo, hi);
+}
+
+// grid: x = ((b * row_tiles + row tile) * H_kv + key head) * splits + split
+template <int D, int MT, bool F16>
+__global__ void __launch_bounds__(kThreads) paged_stream_kernel(const PagedAttnParams p, int row_tiles) {
+    using C = StreamCfg<D, MT>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    grid_dep_launch();
+    const csa_kv_cache& kv = p.kv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned u = blockIdx.x;
+    const int split = (int)(u % (unsigned)p.splits);
+    u /= (unsigned)p.splits;
+    const int hk = (int)(u % (unsigned)kv.H_kv);
+    u /= (unsigned)kv.H_kv;
+    const int rt = (int)(u % (unsigned)row_tiles), b = (int)(u / (unsigned)row_tiles);
+    const int G = kv.H / kv.H_kv;
+
+    // the block's rows r in [0, R): new token (r0 + r) / G of the sequence, head (r0 + r) % G of the group
+    csa_kv_seq seq;
+    const int64_t r0 = (int64_t)rt * C::kRows;
+    int64_t pos0;  // position of the sequence's new token 0
+    if (p.prefix_mode) {
+        seq.row = 0;
+        seq.n = p.rows;
+        pos0 = p.prefix_len;
+    } else {
+        if (!paged_seq(kv, b, p.rows, p.max_n, p.prefix_len, p.status,
+                       threadIdx.x == 0 && rt == 0 && hk == 0 && split == 0, &seq))
+            return;
+        pos0 = seq.len - seq.n;
+    }
+    const int64_t left = seq.n * G - r0;
+    if (left <= 0) return;
+    const int R = (int)(left < C::kRows ? left : C::kRows);
+    const int64_t tok0 = r0 / G, tok1 = (r0 + R - 1) / G;
+    const KeySpan span = key_span(p, pos0 + tok0, tok1 - tok0 + 1);
+    const int p_first = (int)(pos0 + tok0), p_last = (int)(pos0 + tok1);
+    const int32_t* table = kv.page_table + (p.prefix_mode ? 0 : (int64_t)b * kv.max_pages);
+
+    // 16-key groups: those of the first tokens, then those of the window from lo rounded down
+    const int n_first = (span.s1 + 15) >> 4, win0 = span.lo & ~15;
+    const int n_groups = n_first + (span.hi > span.lo ? (span.hi - win0 + 15) >> 4 : 0);
+    const int g_begin = (int)((int64_t)n_groups * split / p.splits);
+    const int g_end = (int)((int64_t)n_groups * (split + 1) / p.splits);
+    const int my = g_end - g_begin > warp ? (g_end - g_begin - warp + kWarps - 1) / kWarps : 0;
+
+    const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
+    const uint16_t* kp = static_cast<const uint16_t*>(kv.k_pages);
+    const uint16_t* vp = static_cast<const uint16_t*>(kv.v_pages);
+    constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte chunks of a row, rows per warp instruction
+    const int c_row = lane / kChunks, c_col = lane % kChunks;
+
+    auto group_start = [&](int g, int* a, int* e) {
+        const bool first = g < n_first;
+        *a = first ? 0 : span.lo;
+        *e = first ? span.s1 : span.hi;
+        return first ? g * 16 : win0 + (g - n_first) * 16;
+    };
+    const int shift = page_shift(kv);
+    auto lookup = [&](int i) {  // page of the warp's group i, or -1
+        if (i >= my) return -1;
+        int a, e;
+        return page_of(kv, table, shift, group_start(g_begin + warp + i * kWarps, &a, &e), p.status);
+    };
+    auto copy = [&](int i, int page) {
+        if (i < my) {
+            int a, e;
+            const int t0 = group_start(g_begin + warp + i * kWarps, &a, &e);
+            const uint32_t dst = ring + (i % C::kStages) * (2 * C::kGroup);
+            const int64_t off = (page < 0 ? 0 : page) * kv.page_stride + hk * kv.head_stride;
+            const int s0 = t0 & (kv.page_size - 1);
+#pragma unroll
+            for (int j = 0; j < 16 / kPer; ++j) {
+                const int key = j * kPer + c_row;
+                const uint32_t n = page >= 0 && t0 + key >= a && t0 + key < e ? 16u : 0u;
+                const int64_t o = n ? off + (s0 + key) * kv.slot_stride + c_col * 8 : 0;
+                const uint32_t at = dst + key * (D * 2) + ((c_col ^ (key & 7)) << 4);
+                cp_async16(at, kp + o, n);
+                cp_async16(at + C::kGroup, vp + o, n);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    int page_next = lookup(0);
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) {
+        const int pg = page_next;
+        page_next = lookup(i + 1);
+        copy(i, pg);
+    }
+
+    // Q as the A operand: rows lane / 4 (+ 8) of each 16-row tile
+    const int ra = lane >> 2, cq = (lane & 3) * 2;
+    uint32_t qf[MT][D / 16][4];
+    int pr[2 * MT];  // positions of this thread's rows
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+        const int r = i * 8 + ra;
+        const int64_t f = r0 + (r < R ? r : 0);
+        const int64_t tok = f / G;
+        const uint16_t* src = p.q + (seq.row + tok) * p.q_stride + (hk * G + (f - tok * G)) * D + cq;
+        pr[i] = (int)(pos0 + tok);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            qf[i >> 1][k][i & 1] = r < R ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
+            qf[i >> 1][k][(i & 1) + 2] = r < R ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
+        }
+    }
+
+    float o[MT][D / 8][4];
+    float m[2 * MT], l[2 * MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+    }
+
+    const int km = lane >> 3, kr = lane & 7;  // ldmatrix: this lane addresses row kr of matrix km
+    for (int i = 0; i < my; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+        __syncwarp();
+        {
+            const int pg = page_next;
+            page_next = lookup(i + C::kStages);
+            copy(i + C::kStages - 1, pg);
+        }
+        const uint32_t kb = ring + (i % C::kStages) * (2 * C::kGroup), vb = kb + C::kGroup;
+        float s[MT][2][4];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[t][n][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            uint32_t kf[4];
+            const int key = (km >> 1) * 8 + kr;
+            ldmatrix4(kb + key * (D * 2) + (((2 * k + (km & 1)) ^ (key & 7)) << 4), kf);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                mma16816<F16>(s[t][0], qf[t][k], kf[0], kf[1]);
+                mma16816<F16>(s[t][1], qf[t][k], kf[2], kf[3]);
+            }
+        }
+        int a, e;
+        const bool first = g_begin + warp + i * kWarps < n_first;
+        const int t0 = group_start(g_begin + warp + i * kWarps, &a, &e);
+        const bool whole = t0 >= a && t0 + 16 <= e &&
+                           (first || (t0 + 15 <= p_first && (t0 > p_last - p.W || t0 + 16 <= p.S)));
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                float x[4] = {s[t][0][2 * hh] * p.scale_log2, s[t][0][2 * hh + 1] * p.scale_log2,
+                              s[t][1][2 * hh] * p.scale_log2, s[t][1][2 * hh + 1] * p.scale_log2};
+                if (!whole) {
+                    const int pos = pr[2 * t + hh];
+                    uint32_t see;
+                    if (first) {
+                        see = span16(t0, 0, span.s1);
+                    } else {  // (a prefix: pos lies behind hi, so all of it)
+                        const int up = pos + 1 < span.hi ? pos + 1 : span.hi;
+                        const int w0 = pos - p.W + 1 > span.lo ? pos - p.W + 1 : span.lo;
+                        see = span16(t0, w0, up) | span16(t0, span.lo, p.S < up ? p.S : up);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (!((see >> (cq + (c & 1) + (c >> 1) * 8)) & 1u)) x[c] = -INFINITY;
+                }
+                float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const int ri = 2 * t + hh;
+                if (__any_sync(0xffffffffu, mx > m[ri])) {
+                    const float mn = fmaxf(m[ri], mx);
+                    const float f = mn == -INFINITY ? 1.f : fast_exp2(m[ri] - mn);
+                    m[ri] = mn;
+                    l[ri] *= f;
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) {
+                        o[t][j][2 * hh] *= f;
+                        o[t][j][2 * hh + 1] *= f;
+                    }
+                }
+                const float mu = m[ri] == -INFINITY ? 0.f : m[ri];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float w = fast_exp2(x[c] - mu);
+                    l[ri] += w;
+                    s[t][c >> 1][2 * hh + (c & 1)] = w;
+                }
+            }
+        }
+        // the weights, rounded to the cache's type, as the A operand of the product with V: the sum l
+        // keeps the unrounded ones (the rounding errors of the keys average out, at most half a step each)
+        uint32_t pf[MT][4];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            pf[t][0] = pack16<F16>(s[t][0][0], s[t][0][1]);
+            pf[t][1] = pack16<F16>(s[t][0][2], s[t][0][3]);
+            pf[t][2] = pack16<F16>(s[t][1][0], s[t][1][1]);
+            pf[t][3] = pack16<F16>(s[t][1][2], s[t][1][3]);
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            uint32_t vf[4];
+            const int key = (km & 1) * 8 + kr;
+            ldmatrix4t(vb + key * (D * 2) + (((2 * j + (km >> 1)) ^ (key & 7)) << 4), vf);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                mma16816<F16>(o[t][2 * j], pf[t], vf[0], vf[1]);
+                mma16816<F16>(o[t][2 * j + 1], pf[t], vf[2], vf[3]);
+            }
+        }
+        __syncwarp();
+    }
+    cp_async_wait_all();
+    __syncwarp();
+
+    // the warps' results meet: each in its own ring
+    float* so = reinterpret_cast<float*>(smem + warp * C::kWarpBytes);
+    float2* ml = reinterpret_cast<float2*>(smem + C::kML);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const int ri = 2 * t + hh, r = t * 16 + hh * 8 + ra;
+            l[ri] += __shfl_xor_sync(0xffffffffu, l[ri], 1);
+            l[ri] += __shfl_xor_sync(0xffffffffu, l[ri], 2);
+            if ((lane & 3) == 0) ml[warp * C::kRows + r] = make_float2(m[ri], l[ri]);
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+                *reinterpret_cast<float2*>(so + r * C::kOStride + j * 8 + cq) =
+                    make_float2(o[t][j][2 * hh], o[t][j][2 * hh + 1]);
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < R * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * C::kRows + r].x);
+        const float mu = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float2 v = ml[w * C::kRows + r];
+            const float f = fast_exp2(v.x - mu);  // 0 for a warp without keys
+            const float4 x = *reinterpret_cast<const float4*>(smem + w * C::kWarpBytes + (r * C::kOStride + c) * 4);
+            sum = fmaf(v.y, f, sum);
+            acc.x = fmaf(x.x, f, acc.x);
+            acc.y = fmaf(x.y, f, acc.y);
+            acc.z = fmaf(x.z, f, acc.z);
+            acc.w = fmaf(x.w, f, acc.w);
+        }
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;  // (a NaN sum stays NaN)
+        acc.x *= inv;
+        acc.y *= inv;
+        acc.z *= inv;
+        acc.w *= inv;
+        const int64_t f = r0 + r, tok = f / G;
+        const int64_t row = seq.row + tok;
+        const int h = hk * G + (int)(f - tok * G);
+        if (p.part_o) {
+            const int64_t at = ((int64_t)(p.part_base + split) * p.rows + row) * kv.H + h;
+            *reinterpret_cast<float4*>(p.part_o + at * D + c) = acc;
+            if (c == 0) p.part_lse[at] = sum == 0.f ? -INFINITY : mu + log2f(sum);
+        } else {
+            *reinterpret_cast<uint2*>(p.out + row * p.out_stride + h * D + c) =
+                make_uint2(pack16<F16>(acc.x, acc.y), pack16<F16>(acc.z, acc.w));
+            if (c == 0 && p.lse)
+                p.lse[row * kv.H + h] = sum == 0.f ? -INFINITY : (mu + log2f(sum)) * 0.69314718055994530942f;
+        }
+    }
+}
+
+// out = sum_s 2^(lse_s - lse) part_s, lse = log2 sum_s 2^(lse_s), over the slots of one (row, head):
+// D / 4 threads each take four channels.  grid: x = ((b * row blocks) + block)
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedAttnParams p, int slots, int blocks) {
+    constexpr int kLanes = D / 4, kHeads = kThreads / kLanes;
+    grid_dep_wait();
+    const csa_kv_cache& kv = p.kv;
+    const int b = (int)(blockIdx.x / (unsigned)blocks);
+    csa_kv_seq seq;
+    if (!paged_seq(kv, b, p.rows, p.max_n, p.prefix_len, nullptr, false, &seq)) return;
+    const int64_t f = (int64_t)(blockIdx.x % (unsigned)blocks) * kHeads + threadIdx.x / kLanes;
+    if (f >= seq.n * kv.H) return;
+    const int c = (threadIdx.x % kLanes) * 4;
+    const int64_t at = seq.row * kv.H + f, step = p.rows * kv.H;
+    float top = -INFINITY;
+    for (int s = 0; s < slots; ++s) top = fmaxf(top, p.part_lse[at + s * step]);
+    const float mu = top == -INFINITY ? 0.f : top;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < slots; ++s) {
+        const float e = p.part_lse[at + s * step];
+        if (e == -INFINITY) continue;  // an empty partial has no output
+        const float w = fast_exp2(e - mu);
+        const float4 x = *reinterpret_cast<const float4*>(p.part_o + (at + s * step) * D + c);
+        sum += w;
+        acc.x = fmaf(x.x, w, acc.x);
+        acc.y = fmaf(x.y, w, acc.y);
+        acc.z = fmaf(x.z, w, acc.z);
+        acc.w = fmaf(x.w, w, acc.w);
+    }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    const int64_t row = seq.row + f / kv.H;
+    const int h = (int)(f % kv.H);
+    *reinterpret_cast<uint2*>(p.out + row * p.out_stride + h * D + c) =
+        make_uint2(pack16<F16>(acc.x * inv, acc.y * inv), pack16<F16>(acc.z * inv, acc.w * inv));
+    if (c == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (mu + log2f(sum)) * 0.69314718055994530942f;
+}
+
+template <int D, int MT, bool F16>
+cudaError_t launch_stream(const PagedAttnParams& p, cudaStream_t stream, bool pdl) {
+    using C = StreamCfg<D, MT>;
+    static PerDeviceOnce once;
+    cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(paged_stream_kernel<D, MT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    C::kTotal);
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t G = p.kv.H / p.kv.H_kv, n = p.prefix_mode ? p.rows : p.max_n;
+    const int64_t row_tiles = (n * G + C::kRows - 1) / C::kRows;
+    const int64_t grid = (p.prefix_mode ? 1 : p.kv.B) * row_tiles * p.kv.H_kv * p.splits;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    return launch_kernel(paged_stream_kernel<D, MT, F16>, dim3((unsigned)grid), dim3(kThreads), C::kTotal, stream,
+                         pdl, p, (int)row_tiles);
+}
+
+template <int D>
+cudaError_t launch_stream_d(const PagedAttnParams& p, cudaStream_t stream, bool pdl) {
+    const int64_t G = p.kv.H / p.kv.H_kv, n = p.prefix_mode ? p.rows : p.max_n;
+    const bool f16 = p.kv.type == CSA_KV_F16;
+    if (n * G <= 16)
+        return f16 ? launch_stream<D, 1, true>(p, stream, pdl) : launch_stream<D, 1, false>(p, stream, pdl);
+    return f16 ? launch_stream<D, 2, true>(p, stream, pdl) : launch_stream<D, 2, false>(p, stream, pdl);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_stream(const PagedAttnParams& p, cudaStream_t stream, bool pdl) {
+    return p.kv.d == 128 ? launch_stream_d<128>(p, stream, pdl) : launch_stream_d<64>(p, stream, pdl);
+}
+
+cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots, cudaStream_t stream, bool pdl) {
+    const int heads = kThreads / (p.kv.d / 4);
+    const int64_t blocks = ((int64_t)p.max_n * p.kv.H + heads - 1) / heads;
+    const int64_t grid = blocks * p.kv.B;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const bool f16 = p.kv.type == CSA_KV_F16;
+    auto k = p.kv.d == 128 ? (f16 ? paged_combine_kernel<128, true> : paged_combine_kernel<128, false>)
+                           : (f16 ? paged_combine_kernel<64, true> : paged_combine_kernel<64, false>);
+    return launch_kernel(k, dim3((unsigned)grid), dim3(kThreads), 0, stream, pdl, p, slots, (int)blocks);
+}
+
+}  // namespace csa

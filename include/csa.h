@@ -321,18 +321,126 @@ typedef struct csa_prefill_args {
  * a workspace smaller than the call's plan is rejected with CSA_ERR_ARG. */
 int hybrid_attn_prefill(const csa_prefill_args* args, void* ws, size_t ws_bytes, csa_stream_t stream);
 
+/* Paged key/value cache of an ordinary attention layer (separate keys and values, H query heads on
+ * H_kv key/value heads, G = H / H_kv), for the local and full-attention layers of a model whose other
+ * layers are the compressed ones above.  A host struct, read during the call; its pointers are device
+ * memory.  Token t of sequence b lies in page page_table[b * max_pages + t / page_size] at slot
+ * t % page_size: element (page, slot, h, c) of a pool is at page * page_stride + slot * slot_stride +
+ * h * head_stride + c, so a page may hold its slots or its heads outermost.
+ *  Supported: d in {64, 128}; 1 <= H <= 256; H_kv divides H; G <= 64; page_size a power of two from 16
+ *  to 256; max_pages * page_size <= 2^30; pools 16-byte aligned and strides positive multiples of 8
+ *  (of head_stride only when H_kv > 1).
+ *  A page of the table that no query of a call can see is not looked up (its entry may hold anything,
+ *  say because the page was given back); slots behind a sequence's end and tokens that left every
+ *  query's window may hold any bits, NaN included.  A page number outside [0, num_pages) where a
+ *  visible token should lie is reported as CSA_ERR_INDEX and its keys and values count as zeros; an
+ *  append skips it. */
+#define CSA_KV_BF16 0
+#define CSA_KV_F16 1
+
+/* One sequence of a call, device memory: its new tokens are the rows [row, row + n) of the call's token
+ * arrays (q, k, v, out, lse), the newest n of the `len` tokens it holds (new ones included): row
+ * row + i is position len - n + i.  n = 0 leaves the sequence out.  Rows that belong to no sequence are
+ * neither read nor written.  An entry with n < 0, n > max_n, len < n, len > max_pages * page_size or
+ * rows outside [0, rows) is reported as CSA_ERR_INDEX and the sequence is skipped. */
+typedef struct csa_kv_seq {
+    int64_t row;
+    int64_t n;
+    int64_t len;
+} csa_kv_seq;
+
+typedef struct csa_kv_cache {
+    int32_t H;            /* query heads */
+    int32_t H_kv;         /* key/value heads */
+    int32_t d;            /* channels of a head */
+    int32_t type;         /* CSA_KV_BF16 or CSA_KV_F16: pages, q, k, v and out */
+    int32_t page_size;    /* tokens of a page */
+    int32_t B;            /* sequences: entries of seqs, rows of page_table */
+    int64_t num_pages;    /* pages of each pool */
+    int64_t max_pages;    /* entries of a row of page_table */
+    int64_t page_stride;  /* strides of the pools, in elements, the same for keys and values */
+    int64_t slot_stride;
+    int64_t head_stride;
+    void* k_pages;
+    void* v_pages;
+    const int32_t* page_table; /* [B, max_pages] */
+    const csa_kv_seq* seqs;    /* [B] */
+} csa_kv_cache;
+
+/* Append with position rotation: for every new token (position t) of every sequence, and every head,
+ *   K[t] = rot(k, t),  V[t] = v,  q_out = rot(q, t)
+ * where rot turns the first `rot` channels in pairs by the angle t * inv_freq[j], j < rot / 2:
+ * (x, y) -> (x cos - y sin, x sin + y cos), on the channels (j, j + rot / 2), or (2 j, 2 j + 1) when
+ * interleaved; the others stay.  The angle is formed and reduced in 64 bits (positions to 2^30), the
+ * turn computed in 32 and rounded once.  q = NULL appends without queries; q_out = q turns them in
+ * place.  rot = 0 copies.  Heads are contiguous: head h of row r at r * stride + h * d.
+ *  Supported: rot a multiple of 16 from 0 to d; 16-byte aligned arrays, strides multiples of 8. */
+typedef struct csa_kv_append_args {
+    csa_kv_cache kv;
+    int64_t rows;        /* rows of the token arrays */
+    int64_t max_n;       /* host bound of every sequence's n */
+    const void* k;       /* [rows, H_kv, d], row stride k_stride */
+    const void* v;       /* [rows, H_kv, d], row stride v_stride */
+    const void* q;       /* [rows, H, d], row stride q_stride; or NULL */
+    void* q_out;         /* [rows, H, d], row stride q_out_stride; with q */
+    int64_t k_stride, v_stride, q_stride, q_out_stride; /* in elements */
+    const float* inv_freq; /* [rot / 2]; may be NULL when rot = 0 */
+    int32_t rot;
+    int32_t interleaved;
+} csa_kv_append_args;
+int csa_kv_append(const csa_kv_append_args* args, csa_stream_t stream);
+
+/* Arguments of csa_window_attn and csa_prefix_attn.  Positions, lengths and rows as in csa_kv_seq; the
+ * new tokens' keys and values are in the cache already (csa_kv_append). */
+typedef struct csa_kv_attn_args {
+    csa_kv_cache kv;
+    int64_t rows;        /* rows of the token arrays */
+    int64_t max_n;       /* host bound of every sequence's n */
+    int64_t max_len;     /* host bound of every sequence's len (sizes the split of long rows) */
+    int64_t W;           /* csa_window_attn: window, >= 1 (the token itself counts); else 0 */
+    int64_t S;           /* csa_window_attn: first tokens that stay visible, >= 0; else 0 */
+    int64_t prefix_len;  /* csa_prefix_attn: tokens of the shared prefix, >= 0; else 0 */
+    float scale;         /* logit scale, > 0 */
+    int32_t reserved;    /* must be 0 */
+    const void* q;       /* [rows, H, d], row stride q_stride (positions already turned) */
+    void* out;           /* [rows, H, d], row stride out_stride, in the cache's type */
+    float* lse;          /* [rows, H] natural log-sum-exp of the scaled logits (nullable) */
+    int64_t q_stride, out_stride; /* in elements; multiples of 8 */
+} csa_kv_attn_args;
+
+/* Causal attention over a sliding window and the first tokens: the query at position p sees every
+ * token t <= p with t > p - W or t < S.  W >= len is plain causal attention.  Any mix of single new
+ * tokens, a few proposed ones, prompts and chunks of prompts.
+ *   out = sum_t softmax_t(scale q . K_t) V_t,  lse = log sum_t exp(scale q . K_t).
+ * Scores, softmax statistics and sums are held in 32 bits; the weights are rounded to the cache's type
+ * for the product with V, the output once at the end.  Workspace: CSA_OP_WINDOW_ATTN; calls that may
+ * run at the same time (two streams, two graphs) need a workspace each. */
+int csa_window_attn(const csa_kv_attn_args* args, void* ws, size_t ws_bytes, csa_stream_t stream);
+
+/* Causal attention (t <= p, no window) of a batch whose sequences share their first prefix_len tokens:
+ * the prefix's keys and values are read through row 0 of the page table, once for all queries of all
+ * sequences, and each sequence's tokens from prefix_len on through its own row; the parts are merged
+ * by log-sum-exp.  prefix_len need not end on a page: the tokens behind it in that page are each
+ * sequence's own, in its own copy of the page.  Every sequence with n > 0 needs len - n >= prefix_len
+ * (else CSA_ERR_INDEX on the device and the sequence is skipped).  Row 0 of the table must hold the
+ * prefix even if its sequence is left out.  Workspace: CSA_OP_PREFIX_ATTN. */
+int csa_prefix_attn(const csa_kv_attn_args* args, void* ws, size_t ws_bytes, csa_stream_t stream);
+
 /* Workspace sizes.  `op` selects the call and `args` points to the arguments it describes:
  *   CSA_OP_INDEX_TOPK:  csa_ws_query {dims, Q, max_len}
  *   CSA_OP_SPARSE_ATTN: csa_ws_query {dims, Q, max_len}
  *   CSA_OP_HCA_ATTN:    csa_ws_query {dims, Q, max_len}
  *   CSA_OP_DECODE:      csa_decode_args
  *   CSA_OP_PREFILL:     csa_prefill_args
+ *   CSA_OP_WINDOW_ATTN, CSA_OP_PREFIX_ATTN: csa_kv_attn_args (its pointers are not looked at)
  * Returns 0 for an unknown op or invalid arguments. */
 #define CSA_OP_INDEX_TOPK 1
 #define CSA_OP_SPARSE_ATTN 2
 #define CSA_OP_HCA_ATTN 3
 #define CSA_OP_DECODE 4
 #define CSA_OP_PREFILL 5
+#define CSA_OP_WINDOW_ATTN 6
+#define CSA_OP_PREFIX_ATTN 7
 
 typedef struct csa_ws_query {
     csa_dims dims;
