@@ -72,13 +72,19 @@ int check_attn(const csa_kv_attn_args& a, int op) {
     return CSA_OK;
 }
 
-// How a call is cut: the partial slots of its launches (1 launch without a split needs none).
+// How a call is cut.  Sequences with few query rows per key head go through the stream kernel, those
+// with more through the tile kernel; so do the rows of all sequences on a shared prefix.
 struct PagedPlan {
-    int splits_window;  // window / suffix launch
-    int splits_prefix;  // prefix launch (0: none)
-    int slots;          // partials per (row, head); 0: written directly
+    bool few, many;              // classes of sequences that may be there
+    int splits_few, splits_many; // key splits of their windows / suffixes
+    bool prefix_tile;
+    int splits_prefix;           // 0: no prefix
+    int slots;                   // partials per (row, head); 0: all written directly
     size_t off_lse, total;
 };
+
+// Rows of one key head up to which the stream kernel is used.
+constexpr int64_t kFewRows = 64;
 
 int sm_count_or(int dflt) {
     int dev = 0, n = 0;
@@ -89,9 +95,9 @@ int sm_count_or(int dflt) {
     return n;
 }
 
-// Splits of a launch of `items` blocks over up to `keys` keys each.
-int plan_splits(int64_t items, int64_t keys, int sms) {
-    const int64_t by_keys = keys / 256 > 1 ? keys / 256 : 1;
+// Splits of a launch of `items` blocks over up to `keys` keys each, at least `least` keys a split.
+int plan_splits(int64_t items, int64_t keys, int64_t least, int sms) {
+    const int64_t by_keys = keys / least > 1 ? keys / least : 1;
     const int64_t by_sms = items > 0 && sms / items > 1 ? sms / items : 1;
     const int64_t s = by_keys < by_sms ? by_keys : by_sms;
     return (int)(s < 256 ? s : 256);
@@ -99,21 +105,30 @@ int plan_splits(int64_t items, int64_t keys, int sms) {
 
 PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
     PagedPlan pl{};
-    const int64_t G = a.kv.H / a.kv.H_kv, cap = a.kv.max_pages * a.kv.page_size;
-    const int64_t max_len = a.max_len < cap ? a.max_len : cap, n = a.max_n < max_len ? a.max_n : max_len;
+    const int64_t G = a.kv.H / a.kv.H_kv, cap = a.kv.max_pages * a.kv.page_size, B = a.kv.B;
+    const int64_t max_len = a.max_len < cap ? a.max_len : cap;
+    int64_t n = a.max_n < max_len ? a.max_n : max_len;
+    if (n > a.rows) n = a.rows;
+    const int64_t n_few = n * G > kFewRows ? kFewRows / G : n, tpb = 2 * (128 / G);
     const int sms = sm_count_or(148);
-    auto row_tiles = [&](int64_t rows) { return (rows * G + 31) / 32; };
-    if (op == CSA_OP_WINDOW_ATTN) {
-        const int64_t win = a.W < max_len ? a.W + n - 1 + (a.S < max_len ? a.S : max_len) : max_len;
-        pl.splits_window = plan_splits(a.kv.B * a.kv.H_kv * row_tiles(n), win < max_len ? win : max_len, sms);
-        pl.slots = pl.splits_window > 1 ? pl.splits_window : 0;
-    } else {
-        const int64_t suffix = max_len > a.prefix_len ? max_len - a.prefix_len : 0;
-        pl.splits_window = plan_splits(a.kv.B * a.kv.H_kv * row_tiles(n), suffix, sms);
-        if (a.prefix_len > 0) pl.splits_prefix = plan_splits(a.kv.H_kv * row_tiles(a.rows), a.prefix_len, sms);
-        pl.slots = pl.splits_window + pl.splits_prefix;
-        if (pl.slots == 1) pl.slots = 0;
+    auto stream_items = [&](int64_t seqs, int64_t rows) { return seqs * a.kv.H_kv * ((rows * G + 31) / 32); };
+    pl.many = n * G > kFewRows;
+    pl.few = !pl.many || B > 1;
+    auto keys = [&](int64_t q) {  // that a block of q queries of one sequence sees
+        if (op == CSA_OP_PREFIX_ATTN) return max_len > a.prefix_len ? max_len - a.prefix_len : (int64_t)0;
+        const int64_t win = a.W < max_len ? a.W + q - 1 + (a.S < max_len ? a.S : max_len) : max_len;
+        return win < max_len ? win : max_len;
+    };
+    if (pl.few) pl.splits_few = plan_splits(stream_items(B, n_few), keys(n_few), 256, sms);
+    if (pl.many) pl.splits_many = plan_splits(B * a.kv.H_kv * ((n + tpb - 1) / tpb), keys(tpb), 512, sms);
+    if (op == CSA_OP_PREFIX_ATTN && a.prefix_len > 0) {
+        pl.prefix_tile = a.rows * G > kFewRows;
+        pl.splits_prefix = pl.prefix_tile
+                               ? plan_splits(a.kv.H_kv * ((a.rows + tpb - 1) / tpb), a.prefix_len, 256, sms)
+                               : plan_splits(stream_items(1, a.rows), a.prefix_len, 256, sms);
     }
+    const int most = pl.splits_few > pl.splits_many ? pl.splits_few : pl.splits_many;
+    pl.slots = pl.splits_prefix || most > 1 ? pl.splits_prefix + most : 0;
     const size_t heads = (size_t)a.rows * a.kv.H * pl.slots;
     pl.off_lse = align256(heads * a.kv.d * 4);
     pl.total = pl.off_lse + align256(heads * 4);
@@ -152,24 +167,36 @@ int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaS
     p.lse = a->lse;
     p.q_stride = a->q_stride;
     p.out_stride = a->out_stride;
-    if (pl.slots) {
-        p.part_o = static_cast<float*>(ws);
-        p.part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + pl.off_lse);
-    }
+    p.few_rows = pl.many ? kFewRows : (int64_t)1 << 40;
+    float* const part_o = static_cast<float*>(ws);
+    float* const part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + pl.off_lse);
     if ((rc = device_status(&p.status))) return rc;
     int fault = 0;
     debug_fault_state(&fault, &p.wait_ns);
-    p.splits = pl.splits_window;
-    cudaError_t e = launch_paged_stream(p, stream);
-    if (e == cudaSuccess && pl.splits_prefix) {
+    // one launch of the queries' prefix, window or suffix part: `splits` partials from slot `base` on, or
+    // directly into out when they are the only ones
+    auto part = [&](bool tile, bool prefix, int base, int splits) {
         PagedAttnParams f = p;
-        f.prefix_mode = 1;
-        f.key_begin = 0;
-        f.splits = pl.splits_prefix;
-        f.part_base = pl.splits_window;
-        e = launch_paged_stream(f, stream);
+        f.prefix_mode = prefix ? 1 : 0;
+        if (prefix) f.key_begin = 0;
+        f.splits = splits;
+        f.part_base = base;
+        if (pl.splits_prefix || splits > 1) {
+            f.part_o = part_o;
+            f.part_lse = part_lse;
+        }
+        return tile ? launch_paged_tile(f, stream) : launch_paged_stream(f, stream);
+    };
+    cudaError_t e = cudaSuccess;
+    if (pl.splits_prefix) e = part(pl.prefix_tile, true, 0, pl.splits_prefix);
+    if (e == cudaSuccess && pl.many) e = part(true, false, pl.splits_prefix, pl.splits_many);
+    if (e == cudaSuccess && pl.few) e = part(false, false, pl.splits_prefix, pl.splits_few);
+    if (e == cudaSuccess && pl.slots) {
+        auto slots = [&](int splits) { return pl.splits_prefix || splits > 1 ? pl.splits_prefix + splits : 0; };
+        p.part_o = part_o;
+        p.part_lse = part_lse;
+        e = launch_paged_combine(p, slots(pl.splits_few), slots(pl.splits_many), stream, true);
     }
-    if (e == cudaSuccess && pl.slots) e = launch_paged_combine(p, pl.slots, stream, true);
     if (e != cudaSuccess) return set_error(CSA_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
     return CSA_OK;
 }

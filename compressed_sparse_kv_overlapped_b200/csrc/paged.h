@@ -41,6 +41,9 @@ struct PagedAttnParams {
     uint16_t* out;
     float* lse;         // nullable
     int64_t q_stride, out_stride;
+    // sequences with n G <= few_rows query rows per key head belong to the stream kernel, the others to
+    // the tile kernel (without prefix_mode)
+    int64_t few_rows;
     // splits of the keys of a block: 1 with part_o = nullptr writes out / lse; otherwise split s of
     // this launch writes the partial slot part_base + s: part_o [slot][rows][H][d] (normalized, fp32),
     // part_lse [slot][rows][H] (base 2; -inf: an empty partial, its part_o is not written)
@@ -53,8 +56,11 @@ struct PagedAttnParams {
 
 // Few query rows per key (decode): mma.sync tiles of 16 or 32 rows, each warp streaming its own keys.
 cudaError_t launch_paged_stream(const PagedAttnParams& p, cudaStream_t stream, bool pdl = false);
-// Merge of `slots` partials per (row, head) into out / lse.
-cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots, cudaStream_t stream, bool pdl);
+// Many query rows per key: tcgen05 tiles of 128 rows.
+cudaError_t launch_paged_tile(const PagedAttnParams& p, cudaStream_t stream);
+// Merge of the partial slots of each (row, head) into out / lse: slots_few of a sequence with few rows,
+// slots_many of another (0: written directly, left alone).
+cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots_few, int slots_many, cudaStream_t stream, bool pdl);
 
 // ---------------------------------------------------------------------------------------------
 

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kThreads) paged_stream_kernel(const PagedAttnP
         if (!paged_seq(kv, b, p.rows, p.max_n, p.prefix_len, p.status,
                        threadIdx.x == 0 && rt == 0 && hk == 0 && split == 0, &seq))
             return;
+        if (seq.n * G > p.few_rows) return;
         pos0 = seq.len - seq.n;
     }
     const int64_t left = seq.n * G - r0;
@@ -355,7 +356,8 @@ __global__ void __launch_bounds__(kThreads) paged_stream_kernel(const PagedAttnP
 // out = sum_s 2^(lse_s - lse) part_s, lse = log2 sum_s 2^(lse_s), over the slots of one (row, head):
 // D / 4 threads each take four channels.  grid: x = ((b * row blocks) + block)
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedAttnParams p, int slots, int blocks) {
+__global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedAttnParams p, int slots_few, int slots_many,
+                                                                int blocks) {
     constexpr int kLanes = D / 4, kHeads = kThreads / kLanes;
     grid_dep_wait();
     const csa_kv_cache& kv = p.kv;
@@ -364,6 +366,8 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedAttn
     if (!paged_seq(kv, b, p.rows, p.max_n, p.prefix_len, nullptr, false, &seq)) return;
     const int64_t f = (int64_t)(blockIdx.x % (unsigned)blocks) * kHeads + threadIdx.x / kLanes;
     if (f >= seq.n * kv.H) return;
+    const int slots = seq.n * (kv.H / kv.H_kv) <= p.few_rows ? slots_few : slots_many;
+    if (slots == 0) return;
     const int c = (threadIdx.x % kLanes) * 4;
     const int64_t at = seq.row * kv.H + f, step = p.rows * kv.H;
     float top = -INFINITY;
@@ -391,6 +395,13 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedAttn
     if (c == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (mu + log2f(sum)) * 0.69314718055994530942f;
 }
 
+// Query rows of one key head, at most.
+int64_t most_rows(const PagedAttnParams& p) {
+    const int64_t G = p.kv.H / p.kv.H_kv;
+    if (p.prefix_mode) return p.rows * G;
+    return p.max_n * G < p.few_rows ? p.max_n * G : p.few_rows;
+}
+
 template <int D, int MT, bool F16>
 cudaError_t launch_stream(const PagedAttnParams& p, cudaStream_t stream, bool pdl) {
     using C = StreamCfg<D, MT>;
@@ -400,8 +411,7 @@ cudaError_t launch_stream(const PagedAttnParams& p, cudaStream_t stream, bool pd
                                     C::kTotal);
     });
     if (e != cudaSuccess) return e;
-    const int64_t G = p.kv.H / p.kv.H_kv, n = p.prefix_mode ? p.rows : p.max_n;
-    const int64_t row_tiles = (n * G + C::kRows - 1) / C::kRows;
+    const int64_t row_tiles = (most_rows(p) + C::kRows - 1) / C::kRows;
     const int64_t grid = (p.prefix_mode ? 1 : p.kv.B) * row_tiles * p.kv.H_kv * p.splits;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     return launch_kernel(paged_stream_kernel<D, MT, F16>, dim3((unsigned)grid), dim3(kThreads), C::kTotal, stream,
@@ -410,9 +420,8 @@ cudaError_t launch_stream(const PagedAttnParams& p, cudaStream_t stream, bool pd
 
 template <int D>
 cudaError_t launch_stream_d(const PagedAttnParams& p, cudaStream_t stream, bool pdl) {
-    const int64_t G = p.kv.H / p.kv.H_kv, n = p.prefix_mode ? p.rows : p.max_n;
     const bool f16 = p.kv.type == CSA_KV_F16;
-    if (n * G <= 16)
+    if (most_rows(p) <= 16)
         return f16 ? launch_stream<D, 1, true>(p, stream, pdl) : launch_stream<D, 1, false>(p, stream, pdl);
     return f16 ? launch_stream<D, 2, true>(p, stream, pdl) : launch_stream<D, 2, false>(p, stream, pdl);
 }
@@ -423,7 +432,8 @@ cudaError_t launch_paged_stream(const PagedAttnParams& p, cudaStream_t stream, b
     return p.kv.d == 128 ? launch_stream_d<128>(p, stream, pdl) : launch_stream_d<64>(p, stream, pdl);
 }
 
-cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots, cudaStream_t stream, bool pdl) {
+cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots_few, int slots_many, cudaStream_t stream,
+                                 bool pdl) {
     const int heads = kThreads / (p.kv.d / 4);
     const int64_t blocks = ((int64_t)p.max_n * p.kv.H + heads - 1) / heads;
     const int64_t grid = blocks * p.kv.B;
@@ -431,7 +441,8 @@ cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots, cudaStream
     const bool f16 = p.kv.type == CSA_KV_F16;
     auto k = p.kv.d == 128 ? (f16 ? paged_combine_kernel<128, true> : paged_combine_kernel<128, false>)
                            : (f16 ? paged_combine_kernel<64, true> : paged_combine_kernel<64, false>);
-    return launch_kernel(k, dim3((unsigned)grid), dim3(kThreads), 0, stream, pdl, p, slots, (int)blocks);
+    return launch_kernel(k, dim3((unsigned)grid), dim3(kThreads), 0, stream, pdl, p, slots_few, slots_many,
+                         (int)blocks);
 }
 
 }  // namespace csa

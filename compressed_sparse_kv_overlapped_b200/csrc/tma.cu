@@ -13,6 +13,17 @@ namespace {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::mutex g_mu;
 
+// The driver's encoder (g_mu held).
+cudaError_t load_encoder() {
+    if (g_encode) return cudaSuccess;
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    cudaError_t err = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
+    if (err != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    return cudaSuccess;
+}
+
 struct Entry {
     const void* base;
     uint64_t inner, rows, pitch;
@@ -37,13 +48,7 @@ cudaError_t tensor_map_2d_bf16(CUtensorMap* out, const void* base, uint64_t inne
             return cudaSuccess;
         }
     }
-    if (!g_encode) {
-        cudaDriverEntryPointQueryResult q;
-        void* fn = nullptr;
-        cudaError_t err = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
-        if (err != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    }
+    if (load_encoder() != cudaSuccess) return cudaErrorNotSupported;
     CUtensorMap m;
     std::memset(&m, 0, sizeof m);
     const cuuint64_t dims[2] = {inner, rows};
@@ -61,6 +66,27 @@ cudaError_t tensor_map_2d_bf16(CUtensorMap* out, const void* base, uint64_t inne
     if (g_used < kCache) ++g_used;
     *out = m;
     return cudaSuccess;
+}
+
+cudaError_t tensor_map_16bit(CUtensorMap* out, bool f16, const void* base, int rank, const uint64_t* dims,
+                             const uint64_t* strides_bytes, const uint32_t* box) {
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        if (load_encoder() != cudaSuccess) return cudaErrorNotSupported;
+    }
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        one[i] = 1;
+        if (i) st[i - 1] = strides_bytes[i - 1];
+    }
+    const CUresult r = g_encode(out, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                                const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace csa

@@ -35,4 +35,9 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
 cudaError_t tensor_map_2d_bf16(CUtensorMap* out, const void* base, uint64_t inner, uint64_t rows,
                                uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_rows, bool swizzle128 = true);
 
+// A tensor map of rank 3 to 5 over bf16 or fp16 with the 128-byte swizzle; strides of dimensions 1 .. in
+// bytes.  Encoded anew by every call (well below a microsecond).
+cudaError_t tensor_map_16bit(CUtensorMap* out, bool f16, const void* base, int rank, const uint64_t* dims,
+                             const uint64_t* strides_bytes, const uint32_t* box);
+
 }  // namespace csa
