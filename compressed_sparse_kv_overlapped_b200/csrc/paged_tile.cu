@@ -22,8 +22,8 @@
 // first scores overlap this one's last product and its epilogue.  Blocks are taken longest first, in
 // alternating order, so that the CTAs' sums stay close for causal prompts.
 //
-// Warps: 0-3 / 4-7 softmax of tile 0 / 1, 8-11 epilogue, 12 MMA issuer, 13 key loader, 14 query
-// loader, 15 zeroing of dead V rows.  Every wait is bounded and winds the CTA down.
+// Warps: 0-3 / 4-7 softmax of tile 0 / 1, 8-11 epilogue, 12 MMA issuer, 13 key loader, 14 look-up of
+// the blocks and query loader, 15 zeroing of dead V rows.  Every wait is bounded and winds the CTA down.
 #include <cfloat>
 
 #include "paged.h"
@@ -36,6 +36,8 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kTile = 128;             // query rows and keys of a tile
 constexpr int kBlk = kTile * 128;      // bytes of 128 rows x 64 channels
+constexpr int kWorks = 4;              // blocks looked up ahead
+constexpr int kReaders = 15;           // warps that read them
 constexpr float kSlack = 8.f;          // base-2 units by which the maximum may pass its reference
 
 struct TileMaps {
@@ -53,7 +55,8 @@ struct TileCfg {
     static constexpr int kOutWarp = 32 * D * 2;
     static constexpr int kMl = kOut + 4 * kOutWarp;         // float2 [2][128]: reference and sum
     static constexpr int kBars = kMl + 2 * kTile * 8;
-    static constexpr int kMisc = kBars + 40 * 8;            // tmem base, abort, block counts of 32 chunks
+    static constexpr int kWork = kBars + 48 * 8;            // TileWork [kWorks]
+    static constexpr int kMisc = kWork + kWorks * 64;       // tmem base, abort, block counts of 32 chunks
     static constexpr int kTotal = kMisc + 8 + 32 * 4;
     static_assert(kTotal <= 227 * 1024, "shared memory of a CTA");
 };
@@ -69,6 +72,7 @@ struct TileBars {
     uint64_t ml_full[2];    // softmax: reference and sum of the block's rows
     uint64_t o_full[2];     // MMA commit: O is complete
     uint64_t o_free[2];     // epilogue: O and the sums are read
+    uint64_t work_full[kWorks], work_empty[kWorks];
     uint64_t fin;
 };
 
@@ -97,17 +101,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-        "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
 // Instruction descriptor of kind::f16, fp32 accumulation, both operands of the cache's type.
 template <bool F16>
 __host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool b_mn_major) {
@@ -134,6 +127,67 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The issue of a product costs more instructions than it has operands if the compiler must move each
+// into uniform registers on its own.  So a warp issues several from one block of code: the operands'
+// descriptors differ in their low words only (addresses below 256 KB: no carry into the other fields),
+// the high word is a constant, TMEM addresses are constants (an allocation of all 512 columns starts
+// at column 0), and the electing predicate is made once per block.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+
+#define CSA_MMA_SS(OFF, P)                                                                     \
+    "add.u32 x, %1, " OFF ";\n\tmov.b64 a, {x, %4};\n\tadd.u32 x, %2, " OFF ";\n\tmov.b64 b, {x, %4};\n\t" \
+    "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, " P ";\n\t"
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred e;\n\t.reg .b32 l;\n\telect.sync l|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// D (+)= A B over 64 channels: K-major operands in shared memory, low descriptor words a and b.
+__device__ __forceinline__ void umma_64ch(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    if (!elect_one()) return;
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 x;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        CSA_MMA_SS("0", "p") CSA_MMA_SS("2", "t") CSA_MMA_SS("4", "t") CSA_MMA_SS("6", "t") "}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"((uint32_t)accumulate)
+        : "memory");
+}
+#define CSA_MMA_TS(I, J, P)                                                                    \
+    "add.u32 x, %1, " I ";\n\tadd.u32 y, %2, " J ";\n\tmov.b64 b, {y, %4};\n\t"                    \
+    "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, " P ";\n\t"
+// D (+)= A B over 32 keys: A in TMEM (8 columns for 16 keys), B MN-major (2048 bytes for 16 keys).
+__device__ __forceinline__ void umma_32keys(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    if (!elect_one()) return;
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        CSA_MMA_TS("0", "0", "p") CSA_MMA_TS("8", "128", "t") "}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"((uint32_t)accumulate)
+        : "memory");
+}
+// The same over the 128 keys of a whole tile.
+__device__ __forceinline__ void umma_128keys(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    if (!elect_one()) return;
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        CSA_MMA_TS("0", "0", "p") CSA_MMA_TS("8", "128", "t") CSA_MMA_TS("16", "256", "t") CSA_MMA_TS("24", "384", "t")
+        CSA_MMA_TS("32", "512", "t") CSA_MMA_TS("40", "640", "t") CSA_MMA_TS("48", "768", "t") CSA_MMA_TS("56", "896", "t")
+        "}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"((uint32_t)accumulate)
+        : "memory");
+}
+#undef CSA_MMA_SS
+#undef CSA_MMA_TS
+
 template <bool F16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     if (F16) {
@@ -153,14 +207,15 @@ __device__ __forceinline__ uint32_t bits32(int from, int to, int base) {
 
 // One block: the tokens [tok0, tok0 + ntok) of a sequence, one key head, key tiles [t0, t1).
 struct TileWork {
-    int b, hk, split;
-    int64_t row0;       // row of the first token
+    int b, hk, split;   // b < 0: there are no more
+    int row0;           // row of the first token
     int p0, ntok;       // its position; tokens (up to 2 tpt)
     int s1, lo, hi;     // visible runs (KeySpan)
     int n_first, win0;  // groups of the first tokens; token where the window's groups start
-    int n_groups;
+    int n_groups, gw;   // groups; of them in a key tile (an even number up to 8)
     int t0, t1;
 };
+static_assert(sizeof(TileWork) <= 64, "an entry of the ring");
 
 struct TileGrid {
     int G, tpt;    // heads of a group; tokens of a 128-row tile
@@ -172,7 +227,7 @@ struct TileGrid {
 __device__ __forceinline__ int seq_blocks(const PagedAttnParams& p, const TileGrid& g, int b, bool say, csa_kv_seq* s) {
     if (!paged_seq(p.kv, b, p.rows, p.max_n, p.prefix_len, p.status, say, s)) return 0;
     if (s->n * g.G <= p.few_rows) return 0;
-    return (int)((s->n + 2 * g.tpt - 1) / (2 * g.tpt));
+    return (int)(((uint32_t)s->n + 2u * g.tpt - 1u) / (2u * g.tpt));  // (n <= rows < 2^30)
 }
 
 // The CTA's k-th block: whole warps call it.  False: there is none.
@@ -180,12 +235,15 @@ __device__ __forceinline__ bool tile_work(const PagedAttnParams& p, const TileGr
                                           TileWork& w) {
     const int64_t at = (int64_t)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     if (at >= g.total) return false;
-    int u = (int)at;
-    w.split = u % p.splits;
-    u /= p.splits;
-    w.hk = u % p.kv.H_kv;
-    u /= p.kv.H_kv;
-    int x = g.total / (p.splits * p.kv.H_kv) - 1 - u;  // the last block of a sequence sees most keys
+    uint32_t u = (uint32_t)at;
+    w.split = 0;
+    if (p.splits > 1) {
+        w.split = (int)(u % (uint32_t)p.splits);
+        u /= (uint32_t)p.splits;
+    }
+    w.hk = (int)(u % (uint32_t)p.kv.H_kv);
+    u /= (uint32_t)p.kv.H_kv;
+    int x = counts[31] - 1 - (int)u;  // the last block of a sequence sees most keys
     int64_t n, row, pos0;
     if (p.prefix_mode) {
         w.b = 0;
@@ -211,7 +269,7 @@ __device__ __forceinline__ bool tile_work(const PagedAttnParams& p, const TileGr
     }
     const int64_t tok0 = (int64_t)x * 2 * g.tpt;
     w.ntok = (int)(n - tok0 < 2 * g.tpt ? n - tok0 : 2 * g.tpt);
-    w.row0 = row + tok0;
+    w.row0 = (int)(row + tok0);
     w.p0 = (int)(pos0 + tok0);
     const KeySpan sp = key_span(p, w.p0, w.ntok);
     w.s1 = sp.s1;
@@ -220,20 +278,26 @@ __device__ __forceinline__ bool tile_work(const PagedAttnParams& p, const TileGr
     w.n_first = (sp.s1 + 15) >> 4;
     w.win0 = sp.lo & ~15;
     w.n_groups = w.n_first + (sp.hi > sp.lo ? (sp.hi - w.win0 + 15) >> 4 : 0);
+    // key tiles of equal width: 12 groups are two tiles of 6, not of 8 and 4 zero ones
     const int T = (w.n_groups + 7) >> 3;
-    w.t0 = (int)((int64_t)T * w.split / p.splits);
-    w.t1 = (int)((int64_t)T * (w.split + 1) / p.splits);
+    w.gw = T > 1 ? (((w.n_groups + T - 1) / T) + 1) & ~1 : (w.n_groups + 1) & ~1;
+    w.t0 = 0;
+    w.t1 = T;
+    if (p.splits > 1) {  // (T < 2^23, at most 256 splits)
+        w.t0 = (int)((uint32_t)T * (uint32_t)w.split / (uint32_t)p.splits);
+        w.t1 = (int)((uint32_t)T * (uint32_t)(w.split + 1) / (uint32_t)p.splits);
+    }
     return true;
 }
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_tile_kernel(const __grid_constant__ TileMaps maps, const PagedAttnParams p) {
+    paged_tile_kernel(const __grid_constant__ TileMaps maps, const __grid_constant__ PagedAttnParams p) {
     using C = TileCfg<D>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_u32(smem);
     TileBars<C::kStages>* bars = reinterpret_cast<TileBars<C::kStages>*>(smem + C::kBars);
-    static_assert(sizeof(*bars) <= 40 * 8, "room for the barriers");
+    static_assert(sizeof(*bars) <= 48 * 8, "room for the barriers");
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
     int* counts = reinterpret_cast<int*>(misc + 2);
@@ -263,6 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&bars->ml_full[i], 4);
                 mbar_init(&bars->o_full[i], 1);
                 mbar_init(&bars->o_free[i], 4);
+            }
+            for (int i = 0; i < kWorks; ++i) {
+                mbar_init(&bars->work_full[i], 1);
+                mbar_init(&bars->work_empty[i], kReaders);
             }
             mbar_init(&bars->fin, 1);
             misc[1] = 0;
@@ -296,93 +364,118 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = misc[0];
+    if (misc[0] != 0) {  // (an allocation of every column starts at the first)
+        if (threadIdx.x == 0) report(p.status, CSA_ERR_CUDA);
+        if (warp == 12) tmem_dealloc(misc[0], 512);
+        return;
+    }
     g.total = counts[31] * kv.H_kv * p.splits;
-    const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
+    // S (and P) of tile q in columns 128 q, O in columns 256 + 128 q
+    auto tS = [&](int q) { return (uint32_t)q * 128u; };
+    auto tO = [&](int q) { return 256u + (uint32_t)q * 128u; };
 
+    // A bounded wait of a whole warp, kept small: the kernel's roles share the instruction cache.  Time in
+    // units of 256 clocks (at most 2 GHz); the first to give up makes every role stop, and the end of the
+    // kernel reports it.
+    const uint32_t limit = (uint32_t)(p.wait_ns >> 7);
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, p.status, abort_flag, p.wait_ns));
+        const uint32_t t0 = (uint32_t)(clock64() >> 8);
+        bool done;
+#pragma unroll 1
+        while (!(done = mbar_try_wait(bar, parity & 1u))) {
+            if (*abort_flag) break;
+            if ((uint32_t)(clock64() >> 8) - t0 > limit) *abort_flag = 2;
+        }
+        return __all_sync(0xffffffffu, done);
     };
+    // the CTA's k-th block, looked up by warp 14 for all roles
+    const TileWork* works = reinterpret_cast<const TileWork*>(smem + C::kWork);
     TileWork w;
+    auto next_work = [&](int k) -> bool {
+        if (!wait(&bars->work_full[k % kWorks], k / kWorks)) return false;
+        w = *reinterpret_cast<const TileWork*>(reinterpret_cast<const unsigned char*>(works) + (k % kWorks) * 64);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->work_empty[k % kWorks]);
+        return w.b >= 0;
+    };
 
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 12) {
             // ---------------------------------------------------------------- MMA issuer
-            constexpr uint32_t id_s = idesc_16<F16>(kTile, kTile, false), id_o = idesc_16<F16>(kTile, D, true);
-            uint32_t unit = 0, nb[2] = {0, 0}, nt[2] = {0, 0};
+            constexpr uint32_t id_o = idesc_16<F16>(kTile, D, true);
+            // blocks and key tiles that ran on the two row tiles; tile 1 may be left out of a block
+            uint32_t unit = 0, nb0 = 0, nb1 = 0, nt0 = 0, nt1 = 0;
             bool ok = true;
-            auto stage = [&](uint32_t u) { return u % C::kStages; };
-            auto phase = [&](uint32_t u) { return u / C::kStages; };
-            auto scores = [&](int q, uint32_t u) {
-                const uint64_t qd = sdesc_kmajor(sbase + C::kQ + q * C::kOperand);
-                const uint64_t kd = sdesc_kmajor(sbase + C::kKV + stage(u) * C::kOperand);
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint64_t off = (uint64_t)(((i >> 2) * kBlk + (i & 3) * 32) >> 4);
-                    umma_bf16(tS[q], qd + off, kd + off, id_s, i != 0);
-                }
-                umma_commit(&bars->s_full[q]);
-            };
-            for (int k = 0; ok && tile_work(p, g, counts, k, w); ++k) {
+            for (int k = 0; ok && next_work(k); ++k) {
                 const int T = w.t1 - w.t0, nq = w.ntok > g.tpt ? 2 : 1;
                 if (T == 0) continue;
-                const uint32_t u0 = unit;
-                unit += 2 * T;
-                ok = wait(&bars->kv_full[stage(u0)], phase(u0));
-                for (int q = 0; ok && q < nq; ++q) {
-                    ok = wait(&bars->q_full[q], nb[q]);
-                    if (!ok) break;
-                    tc_fence_after();
-                    scores(q, u0);
-                    if (T == 1) umma_commit(&bars->q_empty[q]);
-                }
-                if (ok) umma_commit(&bars->kv_empty[stage(u0)]);
-                for (int t = 0; ok && t < T; ++t) {
-                    const uint32_t uv = u0 + 2 * t + 1, uk = uv + 1;
-                    const bool more = t + 1 < T;
-                    ok = wait(&bars->kv_full[stage(uv)], phase(uv)) && wait(&bars->v_ready[stage(uv)], phase(uv));
-                    for (int q = 0; ok && q < nq; ++q) {
-                        ok = wait(&bars->p_full[q], nt[q] + t);
-                        if (ok && t == 0 && nb[q] > 0) ok = wait(&bars->o_free[q], nb[q] - 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t vd = sdesc_mnmajor(sbase + C::kKV + stage(uv) * C::kOperand, kBlk);
+                const uint32_t id_s = idesc_16<F16>(kTile, w.gw * 16, false);
+                // step t: for each row tile the product P V of key tile t - 1, then the scores of tile t,
+                // which take the columns of that P: products run in the order of their issue
+#pragma unroll 1
+                for (int t = 0; ok && t <= T; ++t) {
+                    const uint32_t uk = unit + 2 * t, uv = uk - 1;  // ring units of K(t) and V(t - 1)
+                    const uint32_t ks = uk % C::kStages, vs = uv % C::kStages;
+                    if (t > 0) ok = wait(&bars->kv_full[vs], uv / C::kStages) && wait(&bars->v_ready[vs], uv / C::kStages);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            umma_bf16_ts(tO[q], tS[q] + i * 8, vd + (uint64_t)((i * 16 * 128) >> 4), id_o, t > 0 || i > 0);
-                        if (q == nq - 1) umma_commit(&bars->kv_empty[stage(uv)]);
-                        if (more) {
-                            // S takes the columns of P: products run in the order of their issue
-                            if (q == 0) ok = wait(&bars->kv_full[stage(uk)], phase(uk));
+                    for (int q = 0; q < 2; ++q) {
+                        if (!ok || q >= nq) break;
+                        const uint32_t nb = q ? nb1 : nb0;
+                        if (t > 0) {
+                            ok = wait(&bars->p_full[q], (q ? nt1 : nt0) + t - 1);
+                            if (ok && t == 1 && nb > 0) ok = wait(&bars->o_free[q], nb - 1);
                             if (!ok) break;
                             tc_fence_after();
-                            scores(q, uk);
-                            if (t + 2 == T) umma_commit(&bars->q_empty[q]);
+                            const uint32_t vd = desc_lo(sbase + C::kKV + vs * C::kOperand, kBlk);
+                            if (w.gw == 8) {
+                                umma_128keys(tO(q), tS(q), vd, id_o, t > 1);
+                            } else {
+#pragma unroll 1
+                                for (int i = 0; i < w.gw; i += 2)
+                                    umma_32keys(tO(q), tS(q) + i * 8, vd + i * 128, id_o, t > 1 || i > 0);
+                            }
+                            if (q == nq - 1) umma_commit(&bars->kv_empty[vs]);
+                            if (t == T) umma_commit(&bars->o_full[q]);
                         } else {
-                            umma_commit(&bars->o_full[q]);
+                            ok = wait(&bars->q_full[q], nb);
+                        }
+                        if (t < T) {
+                            if (ok && q == 0) ok = wait(&bars->kv_full[ks], uk / C::kStages);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t qd = desc_lo(sbase + C::kQ + q * C::kOperand, 16);
+                            const uint32_t kd = desc_lo(sbase + C::kKV + ks * C::kOperand, 16);
+#pragma unroll
+                            for (int i = 0; i < C::kHalves; ++i)
+                                umma_64ch(tS(q), qd + i * (kBlk >> 4), kd + i * (kBlk >> 4), id_s, i > 0);
+                            umma_commit(&bars->s_full[q]);
+                            if (q == nq - 1) umma_commit(&bars->kv_empty[ks]);
+                            if (t == T - 1) umma_commit(&bars->q_empty[q]);
                         }
                     }
-                    if (ok && more) umma_commit(&bars->kv_empty[stage(uk)]);
                 }
-                for (int q = 0; q < nq; ++q) {
-                    ++nb[q];
-                    nt[q] += T;
+                unit += 2 * T;
+                ++nb0;
+                nt0 += T;
+                if (nq == 2) {
+                    ++nb1;
+                    nt1 += T;
                 }
             }
             umma_commit(&bars->fin);
-            mbar_wait(&bars->fin, 0, p.status, nullptr, p.wait_ns);
+            mbar_wait(&bars->fin, 0, p.status, nullptr, p.wait_ns);  // (all products are done: TMEM may go)
         } else if (warp == 13) {
             // ---------------------------------------------------------------- keys and values
             const int shift = page_shift(kv), grp = lane & 7, half = (lane >> 3) & 1, val = lane >> 4;
             const bool issue = half < C::kHalves;
             uint32_t unit = 0;
             bool ok = true;
-            for (int k = 0; ok && tile_work(p, g, counts, k, w); ++k) {
+            for (int k = 0; ok && next_work(k); ++k) {
                 const int32_t* table = kv.page_table + (int64_t)w.b * kv.max_pages;
                 auto find = [&](int t, int* slot) {  // page and slot of this lane's group of tile t
-                    const int gi = t * 8 + grp;
-                    if (gi >= w.n_groups || t >= w.t1) {
+                    const int gi = t * w.gw + grp;
+                    if (gi >= w.n_groups || grp >= w.gw || t >= w.t1) {
                         *slot = 0;
                         return -1;
                     }
@@ -399,9 +492,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t st = unit % C::kStages;
                         if (unit >= C::kStages) ok = wait(&bars->kv_empty[st], unit / C::kStages - 1);
                         if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[st], C::kOperand);
+                        if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[st], w.gw * 16 * D * 2);
                         __syncwarp();
-                        if (issue && val == e)
+                        if (issue && val == e && grp < w.gw)
                             tma_load_4d(sbase + C::kKV + st * C::kOperand + half * kBlk + grp * 16 * 128,
                                         e ? &maps.v : &maps.k, half * 64, slot, w.hk, page, &bars->kv_full[st]);
                     }
@@ -412,14 +505,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (uint32_t u = unit > C::kStages ? unit - C::kStages : 0; u < unit; ++u)
                     mbar_wait(&bars->kv_full[u % C::kStages], (u / C::kStages) & 1, nullptr, nullptr, p.wait_ns);
         } else if (warp == 14) {
-            // ---------------------------------------------------------------- queries
-            uint32_t nb[2] = {0, 0};
-            bool ok = true;
-            for (int k = 0; ok && tile_work(p, g, counts, k, w); ++k) {
+            // ---------------------------------------------------------------- blocks and queries
+            uint32_t nb0 = 0, nb1 = 0;
+            bool ok = true, last = false;
+            int made = 0;
+            for (int k = 0; ok; ++k) {
+                // two blocks ahead of their queries: the key loader runs on with them
+                for (; ok && !last && made <= k + 2; ++made) {
+                    if (made >= kWorks) ok = wait(&bars->work_empty[made % kWorks], made / kWorks - 1);
+                    if (!ok) break;
+                    last = !tile_work(p, g, counts, made, w);
+                    if (last) w.b = -1;
+                    if (lane == 0) {
+                        *reinterpret_cast<TileWork*>(smem + C::kWork + (made % kWorks) * 64) = w;
+                        mbar_arrive(&bars->work_full[made % kWorks]);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                w = *reinterpret_cast<const TileWork*>(smem + C::kWork + (k % kWorks) * 64);
+                if (w.b < 0) break;
                 if (w.t1 == w.t0) continue;
                 const int nq = w.ntok > g.tpt ? 2 : 1;
                 for (int q = 0; ok && q < nq; ++q) {
-                    if (nb[q] > 0) ok = wait(&bars->q_empty[q], nb[q] - 1);
+                    const uint32_t before = q ? nb1 : nb0;
+                    if (before > 0) ok = wait(&bars->q_empty[q], before - 1);
                     if (!ok) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&bars->q_full[q], g.G * g.tpt * 128 * C::kHalves);
@@ -429,31 +539,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         (int)(w.row0 + q * g.tpt), &bars->q_full[q]);
                     }
                     __syncwarp();
-                    ++nb[q];
+                    if (q) ++nb1; else ++nb0;
                 }
             }
-            if (!ok)
-                for (int q = 0; q < 2; ++q)
-                    if (nb[q]) mbar_wait(&bars->q_full[q], (nb[q] - 1) & 1, nullptr, nullptr, p.wait_ns);
+            if (!ok) {
+                if (nb0) mbar_wait(&bars->q_full[0], (nb0 - 1) & 1, nullptr, nullptr, p.wait_ns);
+                if (nb1) mbar_wait(&bars->q_full[1], (nb1 - 1) & 1, nullptr, nullptr, p.wait_ns);
+            }
         } else {
             // ---------------------------------------------------------------- dead rows of V
             uint32_t unit = 0;
             bool ok = true;
-            for (int k = 0; ok && tile_work(p, g, counts, k, w); ++k) {
+            for (int k = 0; ok && next_work(k); ++k) {
                 for (int t = w.t0; ok && t < w.t1; ++t, unit += 2) {
                     const uint32_t u = unit + 1, st = u % C::kStages;
                     ok = wait(&bars->kv_full[st], u / C::kStages);
                     if (!ok) break;
                     const uint32_t vb = sbase + C::kKV + st * C::kOperand;
                     bool wrote = false;
-                    for (int j = 0; j < 8; ++j) {
-                        const int gi = t * 8 + j;
+#pragma unroll 1
+                    for (int j = 0; j < w.gw; ++j) {
+                        const int gi = t * w.gw + j;
                         if (gi >= w.n_groups) break;
                         const bool first = gi < w.n_first;
                         const int tok = first ? gi * 16 : w.win0 + (gi - w.n_first) * 16;
                         const int a = first ? 0 : w.lo, e = first ? w.s1 : w.hi;
                         if (tok >= a && tok + 16 <= e) continue;
                         wrote = true;
+#pragma unroll 1
                         for (int i = lane; i < 16 * 8 * C::kHalves; i += 32) {
                             const int r = (i >> 3) & 15, key = tok + r;
                             if (key < a || key >= e)
@@ -474,9 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned char* sp = smem + C::kOut + ew * C::kOutWarp;
         const float2* ml = reinterpret_cast<const float2*>(smem + C::kMl);
         const uint32_t rcp = (65536u + g.G - 1) / g.G;  // r / G = r * rcp >> 16 for r < 128, G <= 64
-        uint32_t nb[2] = {0, 0};
+        uint32_t nb0 = 0, nb1 = 0;
         bool ok = true;
-        for (int k = 0; ok && tile_work(p, g, counts, k, w); ++k) {
+        for (int k = 0; ok && next_work(k); ++k) {
             const int nq = w.ntok > g.tpt ? 2 : 1;
             for (int q = 0; ok && q < nq; ++q) {
                 const int nrow = (w.ntok - q * g.tpt < g.tpt ? w.ntok - q * g.tpt : g.tpt) * g.G;
@@ -484,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r = er + lane, rt = (int)((uint32_t)r * rcp >> 16);
                 float m = -INFINITY, l = 0.f;
                 if (w.t1 > w.t0) {
-                    ok = wait(&bars->ml_full[q], nb[q]);
-                    if (ok) ok = wait(&bars->o_full[q], nb[q]);
+                    const uint32_t before = q ? nb1 : nb0;
+                    ok = wait(&bars->ml_full[q], before) && wait(&bars->o_full[q], before);
                     if (!ok) break;
                     const float2 v = ml[q * kTile + r];
                     m = v.x;
@@ -501,13 +614,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (w.t1 == w.t0) continue;
                 tc_fence_after();
-                const uint32_t to = tO[q] + ((uint32_t)er << 16);
+                const uint32_t to = tO(q) + ((uint32_t)er << 16);
                 // rows of D 16-bit values, or of D / 2 floats in two passes, through shared memory, so
                 // that whole rows go out as contiguous 16-byte vectors
                 constexpr int kRow = D * 2, kVec = kRow / 16, kRowsAt = 32 / kVec;
                 const int passes = p.part_o ? 2 : 1;
+#pragma unroll 1
                 for (int s = 0; s < passes; ++s) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         if (passes == 2 && c / (D / 64) != s) continue;
                         uint32_t x[32];
@@ -555,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 }
-                ++nb[q];
+                if (q) ++nb1; else ++nb0;
             }
         }
     } else {
@@ -563,13 +677,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int q = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tS[q] + lanes, to = tO[q] + lanes;
+        const uint32_t ts = tS(q) + lanes, to = tO(q) + lanes;
         float2* ml = reinterpret_cast<float2*>(smem + C::kMl) + q * kTile;
         const int rt = r / g.G;
         const float sc = p.scale_log2;
         uint32_t nb = 0, nt = 0;
         bool ok = true;
-        for (int k = 0; ok && tile_work(p, g, counts, k, w); ++k) {
+        for (int k = 0; ok && next_work(k); ++k) {
             const int T = w.t1 - w.t0;
             if (T == 0 || w.ntok <= q * g.tpt) continue;
             const int p_first = w.p0 + q * g.tpt, p_last = w.p0 + (w.ntok < (q + 1) * g.tpt ? w.ntok : (q + 1) * g.tpt) - 1;
@@ -579,38 +693,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int low = pos - p.W + 1 > w.lo ? pos - p.W + 1 : w.lo;
             const int first_up = p.S < up ? p.S : up;
             const int all_up = p_first + 1 < w.hi ? p_first + 1 : w.hi;  // tokens every row sees, but for the window
+            const int width = 16 * w.gw;
             float m = -INFINITY;
             uint64_t l2[2] = {0, 0};
             for (int t = 0; t < T; ++t) {
                 ok = wait(&bars->s_full[q], nt + t);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t s[128];
+                uint32_t s[128];  // (chunks of 32 keys; those behind the tile's width stay out)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s + c * 32);
+                for (int c = 0; c < 4; ++c)
+                    if (c * 32 < width) tmem_ld32(ts + c * 32, s + c * 32);
                 tmem_ld_wait();
-                const int i0 = (w.t0 + t) * kTile, tok0 = i0 - wb;
-                const bool whole = i0 + kTile <= w.s1 ||
-                                   (i0 >= 16 * w.n_first && tok0 >= w.lo && tok0 + kTile <= all_up &&
-                                    (tok0 > p_last - p.W || tok0 + kTile <= p.S));
+                const bool wide = width == kTile;
+                const int i0 = (w.t0 + t) * width, tok0 = i0 - wb;
+                const bool whole = i0 + width <= w.s1 ||
+                                   (i0 >= 16 * w.n_first && tok0 >= w.lo && tok0 + width <= all_up &&
+                                    (tok0 > p_last - p.W || tok0 + width <= p.S));
                 if (!whole) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int base = i0 + c * 32;
                         const uint32_t see = bits32(0, w.s1, base) | bits32(wb + low, wb + up, base) |
                                              bits32(wb + w.lo, wb + first_up, base);
+                        if (c * 32 < width && __any_sync(0xffffffffu, see != 0xffffffffu)) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((see >> i) & 1u)) s[c * 32 + i] = 0xff800000u;  // -inf
+                            for (int i = 0; i < 32; ++i)
+                                if (!((see >> i) & 1u)) s[c * 32 + i] = 0xff800000u;  // -inf
+                        }
                     }
                 }
-                float mx[4];
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto chunk_max = [&](int c) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(s[c]), __uint_as_float(s[4 + c]));
+                    for (int i = 0; i < 32; i += 8) {
 #pragma unroll
-                for (int i = 8; i < 128; i += 4) {
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = max3(mx[e], __uint_as_float(s[c * 32 + i + e]), __uint_as_float(s[c * 32 + i + e + 4]));
+                    }
+                };
+                if (wide) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(s[i + c]));
+                    for (int c = 0; c < 4; ++c) chunk_max(c);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c * 32 < width) chunk_max(c);
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if (t == 0) {
@@ -642,12 +770,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t sc2 = pair2(sc, sc), neg2 = pair2(neg, neg);
                 // the weights, rounded to the cache's type for the product with V: the sum keeps the
                 // unrounded ones (the rounding errors of the keys average out, half a step each at most)
+                auto chunk_exp = [&](int c) {
+                    uint32_t pk[16];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int e = h * 64 + i * 2;
+                    for (int i = 0; i < 16; ++i) {
+                        const int e = c * 32 + i * 2;
                         float a, b;
                         unpair2(fma2(pair2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, neg2), &a, &b);
                         a = fast_exp2(a);
@@ -655,7 +782,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l2[i & 1] = add2(l2[i & 1], pair2(a, b));
                         pk[i] = pack16<F16>(a, b);
                     }
-                    tmem_st32(ts + h * 32, pk);
+                    tmem_st16(ts + c * 16, pk);
+                };
+                if (wide) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) chunk_exp(c);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c * 32 < width) chunk_exp(c);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -678,7 +813,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) tmem_dealloc(tmem, 512);
+    if (threadIdx.x == 0 && *abort_flag == 2) report(p.status, CSA_ERR_TIMEOUT);
+    if (warp == 12) tmem_dealloc(misc[0], 512);
 }
 
 template <int D, bool F16>
