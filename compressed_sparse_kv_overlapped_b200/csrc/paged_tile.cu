@@ -24,7 +24,7 @@
 //
 // Warps: 0-3 / 4-7 softmax of tile 0 / 1, 8-11 epilogue, 12 MMA issuer, 13 key loader, 14 look-up of
 // the blocks and query loader, 15 zeroing of dead V rows.  Every wait is bounded and winds the CTA down.
-#include <cfloat>
+#include <cstddef>
 
 #include "paged.h"
 #include "tma.h"
@@ -55,11 +55,30 @@ struct TileCfg {
     static constexpr int kOutWarp = 32 * D * 2;
     static constexpr int kMl = kOut + 4 * kOutWarp;         // float2 [2][128]: reference and sum
     static constexpr int kBars = kMl + 2 * kTile * 8;
-    static constexpr int kWork = kBars + 48 * 8;            // TileWork [kWorks]
+    static constexpr int kWork = kBars + 52 * 8;            // TileWork [kWorks]
     static constexpr int kMisc = kWork + kWorks * 64;       // tmem base, abort, block counts of 32 chunks
     static constexpr int kTotal = kMisc + 8 + 32 * 4;
     static_assert(kTotal <= 227 * 1024, "shared memory of a CTA");
 };
+
+// Barriers by their 32-bit address: an operation is one or two instructions.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity & 1u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 
 template <int ST>
 struct TileBars {
@@ -68,7 +87,8 @@ struct TileBars {
     uint64_t v_ready[ST];   // dead rows of the V tile are zero
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];     // MMA commit: S of the tile is complete (and every product before it)
-    uint64_t p_full[2];     // softmax: P is in TMEM, O is rescaled
+    uint64_t p_half[2];     // softmax: O is rescaled, P of the first 64 keys of a full tile is in TMEM
+    uint64_t p_full[2];     // softmax: all of P is
     uint64_t ml_full[2];    // softmax: reference and sum of the block's rows
     uint64_t o_full[2];     // MMA commit: O is complete
     uint64_t o_free[2];     // epilogue: O and the sums are read
@@ -77,16 +97,16 @@ struct TileBars {
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint64_t* bar) {
+                                            uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        "[%6];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        "[%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
@@ -127,6 +147,38 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 2^x of two numbers (x <= 128) on the FMA pipe: the exponential unit gives 16 results a clock and SM,
+// which is as long as the products of a key tile take at d = 128 and twice that at d = 64, so a share of
+// the weights is computed here.  x = n + f, n the nearest whole number (adding and taking away 1.5 2^23),
+// 2^f by a polynomial of degree 5 over [-1/2, 1/2] whose relative error is equal at its seven extremes
+// (Remez exchange), 2.1e-7 with fp32 arithmetic, like the exponential unit's.  Below -127: 0; a NaN stays one.
+__device__ __forceinline__ void poly_exp2(uint64_t x2, float* ra, float* rb) {
+    float a, b;
+    unpair2(x2, &a, &b);
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(a));
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(b));
+    const uint64_t x = pair2(a, b);
+    const uint64_t t = add2(x, pair2(12582912.f, 12582912.f));
+    const uint64_t n = add2(t, pair2(-12582912.f, -12582912.f));
+    const uint64_t f = fma2(n, pair2(-1.f, -1.f), x);
+    uint64_t r = fma2(f, pair2(1.3276472454890609e-3f, 1.3276472454890609e-3f), pair2(9.675540961325169e-3f, 9.675540961325169e-3f));
+    r = fma2(r, f, pair2(5.550713092088699e-2f, 5.550713092088699e-2f));
+    r = fma2(r, f, pair2(2.4022120237350464e-1f, 2.4022120237350464e-1f));
+    r = fma2(r, f, pair2(6.931469440460205e-1f, 6.931469440460205e-1f));
+    r = fma2(r, f, pair2(1.0000001192092896f, 1.0000001192092896f));
+    float ta, tb;
+    unpair2(t, &ta, &tb);
+    const uint64_t e = pair2(__uint_as_float((__float_as_uint(ta) << 23) + 0x3f800000u),
+                             __uint_as_float((__float_as_uint(tb) << 23) + 0x3f800000u));
+    unpair2(mul2(r, e), ra, rb);
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -149,6 +201,10 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred e;\n\t.reg .b32 l;\n\telect.sync l|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
     return r != 0;
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (elect_one())
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 // D (+)= A B over 64 channels: K-major operands in shared memory, low descriptor words a and b.
 __device__ __forceinline__ void umma_64ch(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
@@ -173,14 +229,13 @@ __device__ __forceinline__ void umma_32keys(uint32_t d_tmem, uint32_t a, uint32_
         "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"((uint32_t)accumulate)
         : "memory");
 }
-// The same over the 128 keys of a whole tile.
-__device__ __forceinline__ void umma_128keys(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+// The same over 64 keys.
+__device__ __forceinline__ void umma_64keys(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
     if (!elect_one()) return;
     asm volatile(
         "{\n\t.reg .pred p, t;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
         "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
         CSA_MMA_TS("0", "0", "p") CSA_MMA_TS("8", "128", "t") CSA_MMA_TS("16", "256", "t") CSA_MMA_TS("24", "384", "t")
-        CSA_MMA_TS("32", "512", "t") CSA_MMA_TS("40", "640", "t") CSA_MMA_TS("48", "768", "t") CSA_MMA_TS("56", "896", "t")
         "}" ::"r"(d_tmem),
         "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"((uint32_t)accumulate)
         : "memory");
@@ -297,11 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_u32(smem);
     TileBars<C::kStages>* bars = reinterpret_cast<TileBars<C::kStages>*>(smem + C::kBars);
-    static_assert(sizeof(*bars) <= 48 * 8, "room for the barriers");
+    static_assert(sizeof(*bars) <= 52 * 8, "room for the barriers");
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
     int* counts = reinterpret_cast<int*>(misc + 2);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the shuffle tells the compiler that a warp's threads take the same branches)
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const csa_kv_cache& kv = p.kv;
     if (sbase & 1023u) {  // (the swizzled layout needs it; the launch gives it)
         if (threadIdx.x == 0) report(p.status, CSA_ERR_CUDA);
@@ -323,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&bars->q_full[i], 1);
                 mbar_init(&bars->q_empty[i], 1);
                 mbar_init(&bars->s_full[i], 1);
+                mbar_init(&bars->p_half[i], 4);
                 mbar_init(&bars->p_full[i], 4);
                 mbar_init(&bars->ml_full[i], 4);
                 mbar_init(&bars->o_full[i], 1);
@@ -375,27 +432,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto tO = [&](int q) { return 256u + (uint32_t)q * 128u; };
 
     // A bounded wait of a whole warp, kept small: the kernel's roles share the instruction cache.  Time in
-    // units of 256 clocks (at most 2 GHz); the first to give up makes every role stop, and the end of the
-    // kernel reports it.
-    const uint32_t limit = (uint32_t)(p.wait_ns >> 7);
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const uint32_t t0 = (uint32_t)(clock64() >> 8);
-        bool done;
+    // clocks (two a nanosecond: at least the limit; 2.1 seconds at most); the first to give up makes every
+    // role stop, and the end of the kernel reports it.
+    const uint32_t limit = p.wait_ns < 2100000000ull ? (uint32_t)(p.wait_ns * 2) : 4200000000u;
+    using Bars = TileBars<C::kStages>;
+#define BAR(field, i) (sbase + (uint32_t)(C::kBars + offsetof(Bars, field)) + 8u * (uint32_t)(i))
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        bool done = try_wait(bar, parity);
+        if (__builtin_expect(!done, 0)) {
+            const uint32_t t0 = (uint32_t)clock();
 #pragma unroll 1
-        while (!(done = mbar_try_wait(bar, parity & 1u))) {
-            if (*abort_flag) break;
-            if ((uint32_t)(clock64() >> 8) - t0 > limit) *abort_flag = 2;
+            while (!(done = try_wait(bar, parity))) {
+                if (*abort_flag) break;
+                if ((uint32_t)clock() - t0 > limit) *abort_flag = 2;
+            }
         }
         return __all_sync(0xffffffffu, done);
+    };
+    auto drain = [&](uint32_t bar, uint32_t parity) {  // copies or products in flight, also after an abort
+        const uint32_t t0 = (uint32_t)clock();
+#pragma unroll 1
+        while (!try_wait(bar, parity))
+            if ((uint32_t)clock() - t0 > limit) break;
     };
     // the CTA's k-th block, looked up by warp 14 for all roles
     const TileWork* works = reinterpret_cast<const TileWork*>(smem + C::kWork);
     TileWork w;
     auto next_work = [&](int k) -> bool {
-        if (!wait(&bars->work_full[k % kWorks], k / kWorks)) return false;
+        if (!wait(BAR(work_full, k % kWorks), k / kWorks)) return false;
         w = *reinterpret_cast<const TileWork*>(reinterpret_cast<const unsigned char*>(works) + (k % kWorks) * 64);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->work_empty[k % kWorks]);
+        if (lane == 0) arrive(BAR(work_empty, k % kWorks));
         return w.b >= 0;
     };
 
@@ -417,31 +484,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; ok && t <= T; ++t) {
                     const uint32_t uk = unit + 2 * t, uv = uk - 1;  // ring units of K(t) and V(t - 1)
                     const uint32_t ks = uk % C::kStages, vs = uv % C::kStages;
-                    if (t > 0) ok = wait(&bars->kv_full[vs], uv / C::kStages) && wait(&bars->v_ready[vs], uv / C::kStages);
+                    if (t > 0) ok = wait(BAR(kv_full, vs), uv / C::kStages) && wait(BAR(v_ready, vs), uv / C::kStages);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         if (!ok || q >= nq) break;
                         const uint32_t nb = q ? nb1 : nb0;
                         if (t > 0) {
-                            ok = wait(&bars->p_full[q], (q ? nt1 : nt0) + t - 1);
-                            if (ok && t == 1 && nb > 0) ok = wait(&bars->o_free[q], nb - 1);
+                            const uint32_t turn = (q ? nt1 : nt0) + t - 1;
+                            const bool full = w.gw == 8;
+                            ok = wait(full ? BAR(p_half, q) : BAR(p_full, q), turn);
+                            if (ok && t == 1 && nb > 0) ok = wait(BAR(o_free, q), nb - 1);
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t vd = desc_lo(sbase + C::kKV + vs * C::kOperand, kBlk);
-                            if (w.gw == 8) {
-                                umma_128keys(tO(q), tS(q), vd, id_o, t > 1);
+                            if (full) {
+                                umma_64keys(tO(q), tS(q), vd, id_o, t > 1);
+                                ok = wait(BAR(p_full, q), turn);
+                                if (!ok) break;
+                                tc_fence_after();
+                                umma_64keys(tO(q), tS(q) + 32, vd + 512, id_o, true);
                             } else {
 #pragma unroll 1
                                 for (int i = 0; i < w.gw; i += 2)
                                     umma_32keys(tO(q), tS(q) + i * 8, vd + i * 128, id_o, t > 1 || i > 0);
                             }
-                            if (q == nq - 1) umma_commit(&bars->kv_empty[vs]);
-                            if (t == T) umma_commit(&bars->o_full[q]);
+                            if (q == nq - 1) commit(BAR(kv_empty, vs));
+                            if (t == T) commit(BAR(o_full, q));
                         } else {
-                            ok = wait(&bars->q_full[q], nb);
+                            ok = wait(BAR(q_full, q), nb);
                         }
                         if (t < T) {
-                            if (ok && q == 0) ok = wait(&bars->kv_full[ks], uk / C::kStages);
+                            if (ok && q == 0) ok = wait(BAR(kv_full, ks), uk / C::kStages);
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t qd = desc_lo(sbase + C::kQ + q * C::kOperand, 16);
@@ -449,9 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < C::kHalves; ++i)
                                 umma_64ch(tS(q), qd + i * (kBlk >> 4), kd + i * (kBlk >> 4), id_s, i > 0);
-                            umma_commit(&bars->s_full[q]);
-                            if (q == nq - 1) umma_commit(&bars->kv_empty[ks]);
-                            if (t == T - 1) umma_commit(&bars->q_empty[q]);
+                            commit(BAR(s_full, q));
+                            if (q == nq - 1) commit(BAR(kv_empty, ks));
+                            if (t == T - 1) commit(BAR(q_empty, q));
                         }
                     }
                 }
@@ -463,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     nt1 += T;
                 }
             }
-            umma_commit(&bars->fin);
-            mbar_wait(&bars->fin, 0, p.status, nullptr, p.wait_ns);  // (all products are done: TMEM may go)
+            commit(BAR(fin, 0));
+            drain(BAR(fin, 0), 0);  // (all products are done: TMEM may go)
         } else if (warp == 13) {
             // ---------------------------------------------------------------- keys and values
             const int shift = page_shift(kv), grp = lane & 7, half = (lane >> 3) & 1, val = lane >> 4;
@@ -490,20 +563,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     next = find(t + 1, &next_slot);
                     for (int e = 0; ok && e < 2; ++e, ++unit) {  // K, then V
                         const uint32_t st = unit % C::kStages;
-                        if (unit >= C::kStages) ok = wait(&bars->kv_empty[st], unit / C::kStages - 1);
+                        if (unit >= C::kStages) ok = wait(BAR(kv_empty, st), unit / C::kStages - 1);
                         if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[st], w.gw * 16 * D * 2);
+                        if (lane == 0) arrive_expect_tx(BAR(kv_full, st), w.gw * 16 * D * 2);
                         __syncwarp();
                         if (issue && val == e && grp < w.gw)
                             tma_load_4d(sbase + C::kKV + st * C::kOperand + half * kBlk + grp * 16 * 128,
-                                        e ? &maps.v : &maps.k, half * 64, slot, w.hk, page, &bars->kv_full[st]);
+                                        e ? &maps.v : &maps.k, half * 64, slot, w.hk, page, BAR(kv_full, st));
                     }
                 }
             }
             __syncwarp();
             if (!ok)  // the CTA gives up: its copies in flight land before it ends
                 for (uint32_t u = unit > C::kStages ? unit - C::kStages : 0; u < unit; ++u)
-                    mbar_wait(&bars->kv_full[u % C::kStages], (u / C::kStages) & 1, nullptr, nullptr, p.wait_ns);
+                    drain(BAR(kv_full, u % C::kStages), (u / C::kStages) & 1);
         } else if (warp == 14) {
             // ---------------------------------------------------------------- blocks and queries
             uint32_t nb0 = 0, nb1 = 0;
@@ -512,13 +585,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; ok; ++k) {
                 // two blocks ahead of their queries: the key loader runs on with them
                 for (; ok && !last && made <= k + 2; ++made) {
-                    if (made >= kWorks) ok = wait(&bars->work_empty[made % kWorks], made / kWorks - 1);
+                    if (made >= kWorks) ok = wait(BAR(work_empty, made % kWorks), made / kWorks - 1);
                     if (!ok) break;
                     last = !tile_work(p, g, counts, made, w);
                     if (last) w.b = -1;
                     if (lane == 0) {
                         *reinterpret_cast<TileWork*>(smem + C::kWork + (made % kWorks) * 64) = w;
-                        mbar_arrive(&bars->work_full[made % kWorks]);
+                        arrive(BAR(work_full, made % kWorks));
                     }
                     __syncwarp();
                 }
@@ -529,22 +602,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int nq = w.ntok > g.tpt ? 2 : 1;
                 for (int q = 0; ok && q < nq; ++q) {
                     const uint32_t before = q ? nb1 : nb0;
-                    if (before > 0) ok = wait(&bars->q_empty[q], before - 1);
+                    if (before > 0) ok = wait(BAR(q_empty, q), before - 1);
                     if (!ok) break;
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(&bars->q_full[q], g.G * g.tpt * 128 * C::kHalves);
+                        arrive_expect_tx(BAR(q_full, q), g.G * g.tpt * 128 * C::kHalves);
 #pragma unroll
                         for (int h = 0; h < C::kHalves; ++h)
                             tma_load_3d(sbase + C::kQ + q * C::kOperand + h * kBlk, &maps.q, h * 64, w.hk * g.G,
-                                        (int)(w.row0 + q * g.tpt), &bars->q_full[q]);
+                                        (int)(w.row0 + q * g.tpt), BAR(q_full, q));
                     }
                     __syncwarp();
                     if (q) ++nb1; else ++nb0;
                 }
             }
             if (!ok) {
-                if (nb0) mbar_wait(&bars->q_full[0], (nb0 - 1) & 1, nullptr, nullptr, p.wait_ns);
-                if (nb1) mbar_wait(&bars->q_full[1], (nb1 - 1) & 1, nullptr, nullptr, p.wait_ns);
+                if (nb0) drain(BAR(q_full, 0), (nb0 - 1) & 1);
+                if (nb1) drain(BAR(q_full, 1), (nb1 - 1) & 1);
             }
         } else {
             // ---------------------------------------------------------------- dead rows of V
@@ -553,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; ok && next_work(k); ++k) {
                 for (int t = w.t0; ok && t < w.t1; ++t, unit += 2) {
                     const uint32_t u = unit + 1, st = u % C::kStages;
-                    ok = wait(&bars->kv_full[st], u / C::kStages);
+                    ok = wait(BAR(kv_full, st), u / C::kStages);
                     if (!ok) break;
                     const uint32_t vb = sbase + C::kKV + st * C::kOperand;
                     bool wrote = false;
@@ -575,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (wrote) fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->v_ready[st]);
+                    if (lane == 0) arrive(BAR(v_ready, st));
                 }
             }
         }
@@ -598,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float m = -INFINITY, l = 0.f;
                 if (w.t1 > w.t0) {
                     const uint32_t before = q ? nb1 : nb0;
-                    ok = wait(&bars->ml_full[q], before) && wait(&bars->o_full[q], before);
+                    ok = wait(BAR(ml_full, q), before) && wait(BAR(o_full, q), before);
                     if (!ok) break;
                     const float2 v = ml[q * kTile + r];
                     m = v.x;
@@ -651,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (s == passes - 1) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars->o_free[q]);
+                        if (lane == 0) arrive(BAR(o_free, q));
                     } else {
                         __syncwarp();
                     }
@@ -679,6 +752,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tS(q) + lanes, to = tO(q) + lanes;
         float2* ml = reinterpret_cast<float2*>(smem + C::kMl) + q * kTile;
+        auto stored = [&](uint32_t bar) {  // this warp's TMEM stores so far are complete
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(bar);
+        };
+        constexpr int kPolyEvery = D == 128 ? 4 : 3;  // of the pairs of weights, one on the FMA pipe
         const int rt = r / g.G;
         const float sc = p.scale_log2;
         uint32_t nb = 0, nt = 0;
@@ -697,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY;
             uint64_t l2[2] = {0, 0};
             for (int t = 0; t < T; ++t) {
-                ok = wait(&bars->s_full[q], nt + t);
+                ok = wait(BAR(s_full, q), nt + t);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t s[128];  // (chunks of 32 keys; those behind the tile's width stay out)
@@ -770,15 +850,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t sc2 = pair2(sc, sc), neg2 = pair2(neg, neg);
                 // the weights, rounded to the cache's type for the product with V: the sum keeps the
                 // unrounded ones (the rounding errors of the keys average out, half a step each at most)
-                auto chunk_exp = [&](int c) {
+                auto chunk_exp = [&](int c, bool poly) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int e = c * 32 + i * 2;
                         float a, b;
-                        unpair2(fma2(pair2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, neg2), &a, &b);
-                        a = fast_exp2(a);
-                        b = fast_exp2(b);
+                        const uint64_t x2 = fma2(pair2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, neg2);
+                        if (poly && i % kPolyEvery == kPolyEvery - 1) {
+                            poly_exp2(x2, &a, &b);
+                        } else {
+                            unpair2(x2, &a, &b);
+                            a = fast_exp2(a);
+                            b = fast_exp2(b);
+                        }
                         l2[i & 1] = add2(l2[i & 1], pair2(a, b));
                         pk[i] = pack16<F16>(a, b);
                     }
@@ -786,27 +871,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 if (wide) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) chunk_exp(c);
+                    for (int c = 0; c < 4; ++c) {
+                        chunk_exp(c, true);
+                        if (c == 1) stored(BAR(p_half, q));  // the product of the first 64 keys can start
+                    }
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (c * 32 < width) chunk_exp(c);
+                        if (c * 32 < width) chunk_exp(c, false);
+                    if (lane == 0) arrive(BAR(p_half, q));
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->p_full[q]);
+                stored(BAR(p_full, q));
             }
             if (!ok) break;
             // (the sums of the block before are read once its O is)
-            if (nb > 0) ok = wait(&bars->o_free[q], nb - 1);
+            if (nb > 0) ok = wait(BAR(o_free, q), nb - 1);
             if (!ok) break;
             float a, b, c, d;
             unpair2(l2[0], &a, &b);
             unpair2(l2[1], &c, &d);
             ml[r] = make_float2(m == -INFINITY ? 0.f : m * sc, (a + b) + (c + d));
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->ml_full[q]);
+            if (lane == 0) arrive(BAR(ml_full, q));
             ++nb;
             nt += T;
         }
@@ -816,6 +902,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *abort_flag == 2) report(p.status, CSA_ERR_TIMEOUT);
     if (warp == 12) tmem_dealloc(misc[0], 512);
 }
+
+#undef BAR
 
 template <int D, bool F16>
 cudaError_t launch_tile(const PagedAttnParams& p, cudaStream_t stream) {
