@@ -147,38 +147,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-// 2^x of two numbers (x <= 128) on the FMA pipe: the exponential unit gives 16 results a clock and SM,
-// which is as long as the products of a key tile take at d = 128 and twice that at d = 64, so a share of
-// the weights is computed here.  x = n + f, n the nearest whole number (adding and taking away 1.5 2^23),
-// 2^f by a polynomial of degree 5 over [-1/2, 1/2] whose relative error is equal at its seven extremes
-// (Remez exchange), 2.1e-7 with fp32 arithmetic, like the exponential unit's.  Below -127: 0; a NaN stays one.
-__device__ __forceinline__ void poly_exp2(uint64_t x2, float* ra, float* rb) {
-    float a, b;
-    unpair2(x2, &a, &b);
-    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(a));
-    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(b));
-    const uint64_t x = pair2(a, b);
-    const uint64_t t = add2(x, pair2(12582912.f, 12582912.f));
-    const uint64_t n = add2(t, pair2(-12582912.f, -12582912.f));
-    const uint64_t f = fma2(n, pair2(-1.f, -1.f), x);
-    uint64_t r = fma2(f, pair2(1.3276472454890609e-3f, 1.3276472454890609e-3f), pair2(9.675540961325169e-3f, 9.675540961325169e-3f));
-    r = fma2(r, f, pair2(5.550713092088699e-2f, 5.550713092088699e-2f));
-    r = fma2(r, f, pair2(2.4022120237350464e-1f, 2.4022120237350464e-1f));
-    r = fma2(r, f, pair2(6.931469440460205e-1f, 6.931469440460205e-1f));
-    r = fma2(r, f, pair2(1.0000001192092896f, 1.0000001192092896f));
-    float ta, tb;
-    unpair2(t, &ta, &tb);
-    const uint64_t e = pair2(__uint_as_float((__float_as_uint(ta) << 23) + 0x3f800000u),
-                             __uint_as_float((__float_as_uint(tb) << 23) + 0x3f800000u));
-    unpair2(mul2(r, e), ra, rb);
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -758,7 +726,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive(bar);
         };
-        constexpr int kPolyEvery = D == 128 ? 4 : 3;  // of the pairs of weights, one on the FMA pipe
         const int rt = r / g.G;
         const float sc = p.scale_log2;
         uint32_t nb = 0, nt = 0;
@@ -850,20 +817,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t sc2 = pair2(sc, sc), neg2 = pair2(neg, neg);
                 // the weights, rounded to the cache's type for the product with V: the sum keeps the
                 // unrounded ones (the rounding errors of the keys average out, half a step each at most)
-                auto chunk_exp = [&](int c, bool poly) {
+                auto chunk_exp = [&](int c) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int e = c * 32 + i * 2;
                         float a, b;
                         const uint64_t x2 = fma2(pair2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, neg2);
-                        if (poly && i % kPolyEvery == kPolyEvery - 1) {
-                            poly_exp2(x2, &a, &b);
-                        } else {
-                            unpair2(x2, &a, &b);
-                            a = fast_exp2(a);
-                            b = fast_exp2(b);
-                        }
+                        unpair2(x2, &a, &b);
+                        a = fast_exp2(a);
+                        b = fast_exp2(b);
                         l2[i & 1] = add2(l2[i & 1], pair2(a, b));
                         pk[i] = pack16<F16>(a, b);
                     }
@@ -872,13 +835,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (wide) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        chunk_exp(c, true);
+                        chunk_exp(c);
                         if (c == 1) stored(BAR(p_half, q));  // the product of the first 64 keys can start
                     }
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (c * 32 < width) chunk_exp(c, false);
+                        if (c * 32 < width) chunk_exp(c);
                     if (lane == 0) arrive(BAR(p_half, q));
                 }
                 stored(BAR(p_full, q));
