@@ -79,6 +79,7 @@ struct PagedPlan {
     int splits_few, splits_many; // key splits of their windows / suffixes
     bool prefix_tile;
     int splits_prefix;           // 0: no prefix
+    int few_groups, prefix_groups;  // 16-key groups of a split of the stream kernel
     int slots;                   // partials per (row, head); 0: all written directly
     size_t off_lse, total;
 };
@@ -103,6 +104,24 @@ int plan_splits(int64_t items, int64_t keys, int64_t least, int sms) {
     return (int)(s < 256 ? s : 256);
 }
 
+// The stream kernel's cut: splits of `groups` 16-key groups each, for `items` blocks that see up to `keys`
+// keys.  Lengths are known on the device only, so a split is a fixed number of keys: a shorter sequence
+// has fewer.  Few blocks are cut until there are kWaves per resident place (two an SM), so that the last
+// ones leave little idle; a block never has more than kMostKeys keys, lest one long sequence outlast the
+// rest of its batch.
+int stream_splits(int64_t items, int64_t keys, int sms, int* groups) {
+    constexpr int64_t kWaves = 4, kLeastKeys = 256, kMostKeys = 8192, kMostSplits = 256;
+    const int64_t places = 2 * (int64_t)sms;
+    int64_t s = items > 0 && items < places ? (kWaves * places + items - 1) / items : 1;
+    if (s > keys / kLeastKeys) s = keys / kLeastKeys;
+    if (s < (keys + kMostKeys - 1) / kMostKeys) s = (keys + kMostKeys - 1) / kMostKeys;
+    if (s > kMostSplits) s = kMostSplits;
+    if (s < 1) s = 1;
+    const int64_t n = keys / 16 + 2;  // (both runs of keys may begin and end inside a group)
+    *groups = (int)((n + s - 1) / s);
+    return (int)((n + *groups - 1) / *groups);
+}
+
 PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
     PagedPlan pl{};
     const int64_t G = a.kv.H / a.kv.H_kv, cap = a.kv.max_pages * a.kv.page_size, B = a.kv.B;
@@ -119,13 +138,13 @@ PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
         const int64_t win = a.W < max_len ? a.W + q - 1 + (a.S < max_len ? a.S : max_len) : max_len;
         return win < max_len ? win : max_len;
     };
-    if (pl.few) pl.splits_few = plan_splits(stream_items(B, n_few), keys(n_few), 256, sms);
+    if (pl.few) pl.splits_few = stream_splits(stream_items(B, n_few), keys(n_few), sms, &pl.few_groups);
     if (pl.many) pl.splits_many = plan_splits(B * a.kv.H_kv * ((n + tpb - 1) / tpb), keys(tpb), 512, sms);
     if (op == CSA_OP_PREFIX_ATTN && a.prefix_len > 0) {
         pl.prefix_tile = a.rows * G > kFewRows;
         pl.splits_prefix = pl.prefix_tile
                                ? plan_splits(a.kv.H_kv * ((a.rows + tpb - 1) / tpb), a.prefix_len, 256, sms)
-                               : plan_splits(stream_items(1, a.rows), a.prefix_len, 256, sms);
+                               : stream_splits(stream_items(1, a.rows), a.prefix_len, sms, &pl.prefix_groups);
     }
     const int most = pl.splits_few > pl.splits_many ? pl.splits_few : pl.splits_many;
     pl.slots = pl.splits_prefix || most > 1 ? pl.splits_prefix + most : 0;
@@ -180,6 +199,7 @@ int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaS
         f.prefix_mode = prefix ? 1 : 0;
         if (prefix) f.key_begin = 0;
         f.splits = splits;
+        f.split_groups = prefix ? pl.prefix_groups : pl.few_groups;
         f.part_base = base;
         if (pl.splits_prefix || splits > 1) {
             f.part_o = part_o;

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace csa {
@@ -48,6 +50,7 @@ struct PagedAttnParams {
     // this launch writes the partial slot part_base + s: part_o [slot][rows][H][d] (normalized, fp32),
     // part_lse [slot][rows][H] (base 2; -inf: an empty partial, its part_o is not written)
     int splits, part_base;
+    int split_groups;   // stream kernel: 16-key groups of a split (split s: [s, s + 1) times these, as far as there are)
     float* part_o;
     float* part_lse;
     int* status;
@@ -58,6 +61,8 @@ struct PagedAttnParams {
 cudaError_t launch_paged_stream(const PagedAttnParams& p, cudaStream_t stream, bool pdl = false);
 // Many query rows per key: tcgen05 tiles of 128 rows.
 cudaError_t launch_paged_tile(const PagedAttnParams& p, cudaStream_t stream);
+// Tensor maps of the pools: boxes of 16 slots x 64 channels of one head and page, 128-byte swizzle.
+cudaError_t paged_kv_maps(const csa_kv_cache& kv, CUtensorMap* k, CUtensorMap* v);
 // Merge of the partial slots of each (row, head) into out / lse: slots_few of a sequence with few rows,
 // slots_many of another (0: written directly, left alone).
 cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots_few, int slots_many, cudaStream_t stream, bool pdl);

@@ -2,34 +2,43 @@
 // and the merge of partial results.
 //
 // With G = H / H_kv query heads per key head a decode step does 4 G d operations per 4 d bytes of key
-// and value, so the kernel is a read of the cache: what matters is bytes in flight and how little a
-// key costs on the way.  A block takes one (sequence, 16 or 32 query rows, key head) and a share of
-// its keys; rows are (token, head of the group) pairs.  Its eight warps are independent streams: warp
-// w takes the 16-key groups w, w + 8, ... of the block's share, copies them through a ring of its own
-// (cp.async, kStages groups ahead, no barrier among warps) and keeps its own running maximum, sum and
-// output, in the online softmax form
+// and value, so the kernel is a read of the cache: what matters is bytes in flight and how few
+// instructions a key costs on the way.  A block takes one (sequence, 16 or 32 query rows, key head) and
+// a share of its keys; rows are (token, head of the group) pairs.  Its four warps are independent streams:
+// warp w takes the 16-key groups w, w + 4, ... of the block's share through a ring of its own (one lane
+// issues a TMA box per 64 channels of K and of V, kStages groups ahead, no barrier among warps) and
+// keeps its own running maximum, sum and output, in the online softmax form
 //     m' = max(m, max_t x_t),  l' = l 2^(m - m') + sum_t 2^(x_t - m'),  o' = o 2^(m - m') + sum_t 2^(x_t - m') V_t
-// with x in base-2 units.  The eight results meet once, in shared memory at the end.
+// with x in base-2 units.  The four results meet once, in shared memory at the end.  Two blocks share an
+// SM, so that one's start and end overlap the other's stream; the key heads of the same tokens are
+// neighbours in the grid, since their rows are neighbours in memory.
 //
 // A 16-key group never crosses a page (pages are multiples of 16 and groups are aligned to 16 tokens),
-// so it costs one page lookup, made one group ahead of its copies.  Keys outside the visible runs are
-// filled with zeros without being read: a freed page or an unwritten slot may hold anything, and a
-// weight of zero does not remove a NaN.  The two products run on mma.sync m16n8k16: the tensor pipe
-// is far from a limit here (32 of them per 8 KiB at d = 128) and tcgen05 would want 128 rows.
-#include <cfloat>
-
+// so it costs one page lookup, made one group ahead of its copy.  A group that straddles the end of a
+// visible run is copied whole; its dead rows of V are zeroed before use (a freed page or an unwritten
+// slot may hold anything, and a weight of zero does not remove a NaN), its dead scores replaced.  A page
+// number out of range becomes a coordinate past the last page, which the copy fills with zeros.  The
+// two products run on mma.sync m16n8k16: the tensor pipe is far from a limit here (32 of them per
+// 8 KiB at d = 128) and tcgen05 would want 128 rows.
 #include "paged.h"
+#include "tma.h"
 
 namespace csa {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kCombineThreads = 256;
+
+struct StreamMaps {
+    CUtensorMap k, v;
+};
 
 template <int D, int MT>
 struct StreamCfg {
     static constexpr int kRows = 16 * MT;
+    static constexpr int kHalves = D / 64;         // boxes of 16 rows x 64 channels (2 KB, 128-byte swizzle)
     static constexpr int kGroup = 16 * D * 2;      // bytes of one group's keys (or values)
     static constexpr int kStages = D == 128 ? 3 : 5;
     static constexpr int kWarpBytes = kStages * 2 * kGroup;
@@ -37,7 +46,9 @@ struct StreamCfg {
     static constexpr int kOBytes = kRows * kOStride * 4;  // a warp's result, in its own ring
     static_assert(kOBytes <= kWarpBytes, "the result fits the ring");
     static constexpr int kML = kWarps * kWarpBytes;  // float2 [kWarps][kRows]: maximum and sum
-    static constexpr int kTotal = kML + kWarps * kRows * 8;
+    static constexpr int kBars = kML + kWarps * kRows * 8;
+    static constexpr int kTotal = kBars + kWarps * kStages * 8;
+    static_assert(2 * (kTotal + 1024) <= 227 * 1024, "two blocks on an SM");
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
@@ -68,19 +79,24 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return pack_bf16x2(lo, hi);
 }
 
-// grid: x = ((b * row_tiles + row tile) * H_kv + key head) * splits + split
+// grid: x = ((b * row_tiles + row tile) * splits + split) * H_kv + key head
 template <int D, int MT, bool F16>
-__global__ void __launch_bounds__(kThreads) paged_stream_kernel(const PagedAttnParams p, int row_tiles) {
+__global__ void __launch_bounds__(kThreads)
+    paged_stream_kernel(const __grid_constant__ StreamMaps maps, const __grid_constant__ PagedAttnParams p, int row_tiles) {
     using C = StreamCfg<D, MT>;
-    extern __shared__ __align__(128) unsigned char smem[];
+    extern __shared__ __align__(1024) unsigned char smem[];
     grid_dep_launch();
     const csa_kv_cache& kv = p.kv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem_u32(smem) & 1023u) {  // (the swizzled boxes need it; the launch gives it)
+        if (threadIdx.x == 0) report(p.status, CSA_ERR_CUDA);
+        return;
+    }
     unsigned u = blockIdx.x;
-    const int split = (int)(u % (unsigned)p.splits);
-    u /= (unsigned)p.splits;
     const int hk = (int)(u % (unsigned)kv.H_kv);
     u /= (unsigned)kv.H_kv;
+    const int split = (int)(u % (unsigned)p.splits);
+    u /= (unsigned)p.splits;
     const int rt = (int)(u % (unsigned)row_tiles), b = (int)(u / (unsigned)row_tiles);
     const int G = kv.H / kv.H_kv;
 
@@ -110,15 +126,25 @@ __global__ void __launch_bounds__(kThreads) paged_stream_kernel(const PagedAttnP
     // 16-key groups: those of the first tokens, then those of the window from lo rounded down
     const int n_first = (span.s1 + 15) >> 4, win0 = span.lo & ~15;
     const int n_groups = n_first + (span.hi > span.lo ? (span.hi - win0 + 15) >> 4 : 0);
-    const int g_begin = (int)((int64_t)n_groups * split / p.splits);
-    const int g_end = (int)((int64_t)n_groups * (split + 1) / p.splits);
+    const int g_begin = split * p.split_groups < n_groups ? split * p.split_groups : n_groups;
+    // (the last split takes the rest, should a sequence be longer than the host's bound)
+    const int g_end = split + 1 < p.splits && g_begin + p.split_groups < n_groups ? g_begin + p.split_groups : n_groups;
     const int my = g_end - g_begin > warp ? (g_end - g_begin - warp + kWarps - 1) / kWarps : 0;
+    if (g_begin == g_end && p.part_o) {  // nothing in this split: empty partials
+        if ((int)threadIdx.x < R) {
+            const int64_t f = r0 + threadIdx.x, tok = f / G;
+            p.part_lse[((int64_t)(p.part_base + split) * p.rows + seq.row + tok) * kv.H + hk * G + (f - tok * G)] = -INFINITY;
+        }
+        return;
+    }
 
     const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
-    const uint16_t* kp = static_cast<const uint16_t*>(kv.k_pages);
-    const uint16_t* vp = static_cast<const uint16_t*>(kv.v_pages);
-    constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte chunks of a row, rows per warp instruction
-    const int c_row = lane / kChunks, c_col = lane % kChunks;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars) + warp * C::kStages;
+    if (lane == 0) {
+        for (int i = 0; i < C::kStages; ++i) mbar_init(full + i, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
 
     auto group_start = [&](int g, int* a, int* e) {
         const bool first = g < n_first;
@@ -127,37 +153,33 @@ __global__ void __launch_bounds__(kThreads) paged_stream_kernel(const PagedAttnP
         return first ? g * 16 : win0 + (g - n_first) * 16;
     };
     const int shift = page_shift(kv);
-    auto lookup = [&](int i) {  // page of the warp's group i, or -1
+    auto lookup = [&](int i) {  // page of the warp's group i (past the last: zeros)
         if (i >= my) return -1;
         int a, e;
-        return page_of(kv, table, shift, group_start(g_begin + warp + i * kWarps, &a, &e), p.status);
+        const int pg = page_of(kv, table, shift, group_start(g_begin + warp + i * kWarps, &a, &e), p.status);
+        return pg < 0 ? (int)kv.num_pages : pg;
     };
-    auto copy = [&](int i, int page) {
-        if (i < my) {
-            int a, e;
-            const int t0 = group_start(g_begin + warp + i * kWarps, &a, &e);
-            const uint32_t dst = ring + (i % C::kStages) * (2 * C::kGroup);
-            const int64_t off = (page < 0 ? 0 : page) * kv.page_stride + hk * kv.head_stride;
-            const int s0 = t0 & (kv.page_size - 1);
+    auto copy = [&](int i, int page) {  // by lane 0
+        if (i >= my) return;
+        int a, e;
+        const int slot = group_start(g_begin + warp + i * kWarps, &a, &e) & (kv.page_size - 1), st = i % C::kStages;
+        const uint32_t dst = ring + st * (2 * C::kGroup), bar = smem_u32(full + st);
+        mbar_arrive_expect_tx(full + st, 2 * C::kGroup);
 #pragma unroll
-            for (int j = 0; j < 16 / kPer; ++j) {
-                const int key = j * kPer + c_row;
-                const uint32_t n = page >= 0 && t0 + key >= a && t0 + key < e ? 16u : 0u;
-                const int64_t o = n ? off + (s0 + key) * kv.slot_stride + c_col * 8 : 0;
-                const uint32_t at = dst + key * (D * 2) + ((c_col ^ (key & 7)) << 4);
-                cp_async16(at, kp + o, n);
-                cp_async16(at + C::kGroup, vp + o, n);
-            }
+        for (int h = 0; h < C::kHalves; ++h) {
+            tma_load_4d(dst + h * 2048, &maps.k, h * 64, slot, hk, page, bar);
+            tma_load_4d(dst + C::kGroup + h * 2048, &maps.v, h * 64, slot, hk, page, bar);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    int page_next = lookup(0);
+    int page_next = -1;
+    if (lane == 0) {
+        int pages[C::kStages];
 #pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) {
-        const int pg = page_next;
-        page_next = lookup(i + 1);
-        copy(i, pg);
+        for (int i = 0; i < C::kStages; ++i) pages[i] = lookup(i);
+#pragma unroll
+        for (int i = 0; i < C::kStages; ++i) copy(i, pages[i]);
+        page_next = lookup(C::kStages);
     }
 
     // Q as the A operand: rows lane / 4 (+ 8) of each 16-row tile
@@ -193,15 +215,24 @@ __global__ void __launch_bounds__(kThreads) paged_stream_kernel(const PagedAttnP
     }
 
     const int km = lane >> 3, kr = lane & 7;  // ldmatrix: this lane addresses row kr of matrix km
-    for (int i = 0; i < my; ++i) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-        __syncwarp();
-        {
-            const int pg = page_next;
-            page_next = lookup(i + C::kStages);
-            copy(i + C::kStages - 1, pg);
+    int stage = 0;
+    uint32_t phase = 0;
+    int done = 0;
+    for (; done < my; ++done) {
+        const int i = done;
+        if (!__all_sync(0xffffffffu, mbar_wait(full + stage, phase, p.status, nullptr, p.wait_ns))) break;
+        const uint32_t kb = ring + stage * (2 * C::kGroup), vb = kb + C::kGroup;
+        int a, e;
+        const bool first = g_begin + warp + i * kWarps < n_first;
+        const int t0 = group_start(g_begin + warp + i * kWarps, &a, &e);
+        if (t0 < a || t0 + 16 > e) {
+            for (int c = lane; c < 16 * 8 * C::kHalves; c += 32) {
+                const int r = (c >> 3) & 15;
+                if (t0 + r < a || t0 + r >= e) st_shared_v4(vb + (c >> 7) * 2048 + r * 128 + (c & 7) * 16, make_uint4(0, 0, 0, 0));
+            }
+            fence_proxy_async_smem();  // (the next copy into this stage comes after these stores)
+            __syncwarp();
         }
-        const uint32_t kb = ring + (i % C::kStages) * (2 * C::kGroup), vb = kb + C::kGroup;
         float s[MT][2][4];
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -213,16 +244,13 @@ __global__ void __launch_bounds__(kThreads) paged_stream_kernel(const PagedAttnP
         for (int k = 0; k < D / 16; ++k) {
             uint32_t kf[4];
             const int key = (km >> 1) * 8 + kr;
-            ldmatrix4(kb + key * (D * 2) + (((2 * k + (km & 1)) ^ (key & 7)) << 4), kf);
+            ldmatrix4(kb + (k >> 2) * 2048 + key * 128 + (((2 * (k & 3) + (km & 1)) ^ (key & 7)) << 4), kf);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 mma16816<F16>(s[t][0], qf[t][k], kf[0], kf[1]);
                 mma16816<F16>(s[t][1], qf[t][k], kf[2], kf[3]);
             }
         }
-        int a, e;
-        const bool first = g_begin + warp + i * kWarps < n_first;
-        const int t0 = group_start(g_begin + warp + i * kWarps, &a, &e);
         const bool whole = t0 >= a && t0 + 16 <= e &&
                            (first || (t0 + 15 <= p_first && (t0 > p_last - p.W || t0 + 16 <= p.S)));
 #pragma unroll
@@ -283,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) paged_stream_kernel(const PagedAttnP
         for (int j = 0; j < D / 16; ++j) {
             uint32_t vf[4];
             const int key = (km & 1) * 8 + kr;
-            ldmatrix4t(vb + key * (D * 2) + (((2 * j + (km >> 1)) ^ (key & 7)) << 4), vf);
+            ldmatrix4t(vb + (j >> 2) * 2048 + key * 128 + (((2 * (j & 3) + (km >> 1)) ^ (key & 7)) << 4), vf);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 mma16816<F16>(o[t][2 * j], pf[t], vf[0], vf[1]);
@@ -291,8 +319,19 @@ __global__ void __launch_bounds__(kThreads) paged_stream_kernel(const PagedAttnP
             }
         }
         __syncwarp();
+        if (lane == 0) {
+            const int pg = page_next;
+            page_next = lookup(i + C::kStages + 1);
+            copy(i + C::kStages, pg);
+        }
+        if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
     }
-    cp_async_wait_all();
+    // (after a wait that ran out: copies in flight land before the ring is used again)
+    for (int i = done + 1; done < my && i < my && i < done + C::kStages; ++i)
+        mbar_wait(full + i % C::kStages, (i / C::kStages) & 1, nullptr, nullptr, p.wait_ns);
     __syncwarp();
 
     // the warps' results meet: each in its own ring
@@ -356,9 +395,9 @@ __global__ void __launch_bounds__(kThreads) paged_stream_kernel(const PagedAttnP
 // out = sum_s 2^(lse_s - lse) part_s, lse = log2 sum_s 2^(lse_s), over the slots of one (row, head):
 // D / 4 threads each take four channels.  grid: x = ((b * row blocks) + block)
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedAttnParams p, int slots_few, int slots_many,
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedAttnParams p, int slots_few, int slots_many,
                                                                 int blocks) {
-    constexpr int kLanes = D / 4, kHeads = kThreads / kLanes;
+    constexpr int kLanes = D / 4, kHeads = kCombineThreads / kLanes;
     grid_dep_wait();
     const csa_kv_cache& kv = p.kv;
     const int b = (int)(blockIdx.x / (unsigned)blocks);
@@ -368,24 +407,31 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedAttn
     if (f >= seq.n * kv.H) return;
     const int slots = seq.n * (kv.H / kv.H_kv) <= p.few_rows ? slots_few : slots_many;
     if (slots == 0) return;
-    const int c = (threadIdx.x % kLanes) * 4;
+    const int ln = threadIdx.x % kLanes, c = ln * 4;
     const int64_t at = seq.row * kv.H + f, step = p.rows * kv.H;
+    // a head's lanes read the sums of kLanes slots at once and pass them round
+    const unsigned mask = kLanes == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
     float top = -INFINITY;
-    for (int s = 0; s < slots; ++s) top = fmaxf(top, p.part_lse[at + s * step]);
+    for (int s = ln; s < slots; s += kLanes) top = fmaxf(top, p.part_lse[at + s * step]);
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, o, kLanes));
     const float mu = top == -INFINITY ? 0.f : top;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < slots; ++s) {
-        const float e = p.part_lse[at + s * step];
-        if (e == -INFINITY) continue;  // an empty partial has no output
-        const float w = fast_exp2(e - mu);
-        const float4 x = *reinterpret_cast<const float4*>(p.part_o + (at + s * step) * D + c);
-        sum += w;
-        acc.x = fmaf(x.x, w, acc.x);
-        acc.y = fmaf(x.y, w, acc.y);
-        acc.z = fmaf(x.z, w, acc.z);
-        acc.w = fmaf(x.w, w, acc.w);
+    for (int base = 0; base < slots; base += kLanes) {
+        const float mine = base + ln < slots ? fast_exp2(p.part_lse[at + (base + ln) * step] - mu) : 0.f;
+        const int cnt = slots - base < kLanes ? slots - base : kLanes;
+#pragma unroll 8
+        for (int j = 0; j < cnt; ++j) {
+            const float w = __shfl_sync(mask, mine, j, kLanes);
+            if (w == 0.f) continue;  // (an empty partial has no output)
+            const float4 x = *reinterpret_cast<const float4*>(p.part_o + (at + (base + j) * step) * D + c);
+            sum += w;
+            acc.x = fmaf(x.x, w, acc.x);
+            acc.y = fmaf(x.y, w, acc.y);
+            acc.z = fmaf(x.z, w, acc.z);
+            acc.w = fmaf(x.w, w, acc.w);
+        }
     }
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
     const int64_t row = seq.row + f / kv.H;
@@ -414,8 +460,10 @@ cudaError_t launch_stream(const PagedAttnParams& p, cudaStream_t stream, bool pd
     const int64_t row_tiles = (most_rows(p) + C::kRows - 1) / C::kRows;
     const int64_t grid = (p.prefix_mode ? 1 : p.kv.B) * row_tiles * p.kv.H_kv * p.splits;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    StreamMaps maps;
+    if ((e = paged_kv_maps(p.kv, &maps.k, &maps.v)) != cudaSuccess) return e;
     return launch_kernel(paged_stream_kernel<D, MT, F16>, dim3((unsigned)grid), dim3(kThreads), C::kTotal, stream,
-                         pdl, p, (int)row_tiles);
+                         pdl, maps, p, (int)row_tiles);
 }
 
 template <int D>
@@ -434,14 +482,14 @@ cudaError_t launch_paged_stream(const PagedAttnParams& p, cudaStream_t stream, b
 
 cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots_few, int slots_many, cudaStream_t stream,
                                  bool pdl) {
-    const int heads = kThreads / (p.kv.d / 4);
+    const int heads = kCombineThreads / (p.kv.d / 4);
     const int64_t blocks = ((int64_t)p.max_n * p.kv.H + heads - 1) / heads;
     const int64_t grid = blocks * p.kv.B;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const bool f16 = p.kv.type == CSA_KV_F16;
     auto k = p.kv.d == 128 ? (f16 ? paged_combine_kernel<128, true> : paged_combine_kernel<128, false>)
                            : (f16 ? paged_combine_kernel<64, true> : paged_combine_kernel<64, false>);
-    return launch_kernel(k, dim3((unsigned)grid), dim3(kThreads), 0, stream, pdl, p, slots_few, slots_many,
+    return launch_kernel(k, dim3((unsigned)grid), dim3(kCombineThreads), 0, stream, pdl, p, slots_few, slots_many,
                          (int)blocks);
 }
 

@@ -96,20 +96,6 @@ struct TileBars {
     uint64_t fin;
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-
 // 32 lanes x 32 bits, 32 consecutive columns.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
     asm volatile(
@@ -879,16 +865,10 @@ cudaError_t launch_tile(const PagedAttnParams& p, cudaStream_t stream) {
     const csa_kv_cache& kv = p.kv;
     const int G = kv.H / kv.H_kv, tpt = kTile / G;
     TileMaps maps;
-    const uint64_t row = (uint64_t)kv.slot_stride * 2;
     const uint64_t qd[3] = {(uint64_t)D, (uint64_t)kv.H, (uint64_t)p.rows}, qs[2] = {(uint64_t)D * 2, (uint64_t)p.q_stride * 2};
     const uint32_t qb[3] = {64, (uint32_t)G, (uint32_t)tpt};
-    const uint64_t kd[4] = {(uint64_t)D, (uint64_t)kv.page_size, (uint64_t)kv.H_kv, (uint64_t)kv.num_pages};
-    const uint64_t ks[3] = {row, kv.H_kv > 1 ? (uint64_t)kv.head_stride * 2 : row,
-                            kv.num_pages > 1 ? (uint64_t)kv.page_stride * 2 : row};
-    const uint32_t kb[4] = {64, 16, 1, 1};
     if ((e = tensor_map_16bit(&maps.q, F16, p.q, 3, qd, qs, qb)) != cudaSuccess) return e;
-    if ((e = tensor_map_16bit(&maps.k, F16, kv.k_pages, 4, kd, ks, kb)) != cudaSuccess) return e;
-    if ((e = tensor_map_16bit(&maps.v, F16, kv.v_pages, 4, kd, ks, kb)) != cudaSuccess) return e;
+    if ((e = paged_kv_maps(kv, &maps.k, &maps.v)) != cudaSuccess) return e;
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
@@ -900,6 +880,17 @@ cudaError_t launch_tile(const PagedAttnParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t paged_kv_maps(const csa_kv_cache& kv, CUtensorMap* k, CUtensorMap* v) {
+    const uint64_t row = (uint64_t)kv.slot_stride * 2;
+    const uint64_t dims[4] = {(uint64_t)kv.d, (uint64_t)kv.page_size, (uint64_t)kv.H_kv, (uint64_t)kv.num_pages};
+    const uint64_t strides[3] = {row, kv.H_kv > 1 ? (uint64_t)kv.head_stride * 2 : row,
+                                 kv.num_pages > 1 ? (uint64_t)kv.page_stride * 2 : row};
+    const uint32_t box[4] = {64, 16, 1, 1};
+    const bool f16 = kv.type == CSA_KV_F16;
+    const cudaError_t e = tensor_map_16bit(k, f16, kv.k_pages, 4, dims, strides, box);
+    return e != cudaSuccess ? e : tensor_map_16bit(v, f16, kv.v_pages, 4, dims, strides, box);
+}
 
 cudaError_t launch_paged_tile(const PagedAttnParams& p, cudaStream_t stream) {
     const bool f16 = p.kv.type == CSA_KV_F16;

@@ -35,6 +35,22 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
 cudaError_t tensor_map_2d_bf16(CUtensorMap* out, const void* base, uint64_t inner, uint64_t rows,
                                uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_rows, bool swizzle128 = true);
 
+// Boxes of three and four dimensions; `bar` is the barrier's shared-memory address.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
 // A tensor map of rank 3 to 5 over bf16 or fp16 with the 128-byte swizzle; strides of dimensions 1 .. in
 // bytes.  Encoded anew by every call (well below a microsecond).
 cudaError_t tensor_map_16bit(CUtensorMap* out, bool f16, const void* base, int rank, const uint64_t* dims,
