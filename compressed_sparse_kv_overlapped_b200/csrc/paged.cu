@@ -86,6 +86,7 @@ struct PagedPlan {
 
 // Rows of one key head up to which the stream kernel is used.
 constexpr int64_t kFewRows = 64;
+constexpr int64_t kFewPrefixRows = 64;  // the same for the rows of all sequences on the prefix
 
 int sm_count_or(int dflt) {
     int dev = 0, n = 0;
@@ -96,12 +97,23 @@ int sm_count_or(int dflt) {
     return n;
 }
 
-// Splits of a launch of `items` blocks over up to `keys` keys each, at least `least` keys a split.
-int plan_splits(int64_t items, int64_t keys, int64_t least, int sms) {
-    const int64_t by_keys = keys / least > 1 ? keys / least : 1;
-    const int64_t by_sms = items > 0 && sms / items > 1 ? sms / items : 1;
-    const int64_t s = by_keys < by_sms ? by_keys : by_sms;
-    return (int)(s < 256 ? s : 256);
+// The tile kernel's cut of `items` blocks over up to `keys` keys each: one CTA an SM works them off in
+// rounds.  With few rounds the last one may leave most SMs idle; cutting the keys of every block in s
+// makes the rounds shorter, at a cost of partials (a split has 512 keys at least).
+int tile_splits(int64_t items, int64_t keys, int sms) {
+    if (items <= 0) return 1;
+    int best = 1;
+    double best_time = 1e30;
+    for (int64_t s = 1; s == 1 || (s <= 64 && s * 512 <= keys); ++s) {
+        const double rounds = (double)((items * s + sms - 1) / sms);
+        const double t = rounds / (double)s * (s > 1 ? 1.08 : 1.0) * (1.0 + 0.01 * (double)s);
+        if (t < best_time) {
+            best_time = t;
+            best = (int)s;
+        }
+        if (rounds >= 8.0) break;
+    }
+    return best;
 }
 
 // The stream kernel's cut: splits of `groups` 16-key groups each, for `items` blocks that see up to `keys`
@@ -139,11 +151,15 @@ PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
         return win < max_len ? win : max_len;
     };
     if (pl.few) pl.splits_few = stream_splits(stream_items(B, n_few), keys(n_few), sms, &pl.few_groups);
-    if (pl.many) pl.splits_many = plan_splits(B * a.kv.H_kv * ((n + tpb - 1) / tpb), keys(tpb), 512, sms);
+    if (pl.many) {
+        int64_t blocks = B * ((n + tpb - 1) / tpb);
+        if (blocks > a.rows / tpb + B) blocks = a.rows / tpb + B;
+        pl.splits_many = tile_splits(blocks * a.kv.H_kv, keys(tpb), sms);
+    }
     if (op == CSA_OP_PREFIX_ATTN && a.prefix_len > 0) {
-        pl.prefix_tile = a.rows * G > kFewRows;
+        pl.prefix_tile = a.rows * G > kFewPrefixRows;
         pl.splits_prefix = pl.prefix_tile
-                               ? plan_splits(a.kv.H_kv * ((a.rows + tpb - 1) / tpb), a.prefix_len, 256, sms)
+                               ? tile_splits(a.kv.H_kv * ((a.rows + tpb - 1) / tpb), a.prefix_len, sms)
                                : stream_splits(stream_items(1, a.rows), a.prefix_len, sms, &pl.prefix_groups);
     }
     const int most = pl.splits_few > pl.splits_many ? pl.splits_few : pl.splits_many;
@@ -192,25 +208,37 @@ int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaS
     if ((rc = device_status(&p.status))) return rc;
     int fault = 0;
     debug_fault_state(&fault, &p.wait_ns);
-    // one launch of the queries' prefix, window or suffix part: `splits` partials from slot `base` on, or
-    // directly into out when they are the only ones
-    auto part = [&](bool tile, bool prefix, int base, int splits) {
+    // the rows' parts: partials from slot `base` on, or directly into out when they are the only ones
+    auto tile = [&](bool prefix, int base, int splits) {
         PagedAttnParams f = p;
         f.prefix_mode = prefix ? 1 : 0;
         if (prefix) f.key_begin = 0;
         f.splits = splits;
-        f.split_groups = prefix ? pl.prefix_groups : pl.few_groups;
         f.part_base = base;
         if (pl.splits_prefix || splits > 1) {
             f.part_o = part_o;
             f.part_lse = part_lse;
         }
-        return tile ? launch_paged_tile(f, stream) : launch_paged_stream(f, stream);
+        return launch_paged_tile(f, stream);
     };
     cudaError_t e = cudaSuccess;
-    if (pl.splits_prefix) e = part(pl.prefix_tile, true, 0, pl.splits_prefix);
-    if (e == cudaSuccess && pl.many) e = part(true, false, pl.splits_prefix, pl.splits_many);
-    if (e == cudaSuccess && pl.few) e = part(false, false, pl.splits_prefix, pl.splits_few);
+    PagedStreamParts parts{};
+    auto stream_part = [&](bool prefix, int base, int splits, int groups) {
+        parts.part[parts.n++] = PagedStreamPart{prefix ? 1 : 0, prefix ? 0 : p.key_begin, splits, base, groups, 0,
+                                                pl.splits_prefix || splits > 1};
+    };
+    if (pl.splits_prefix) {
+        if (pl.prefix_tile) e = tile(true, 0, pl.splits_prefix);
+        else stream_part(true, 0, pl.splits_prefix, pl.prefix_groups);
+    }
+    if (e == cudaSuccess && pl.many) e = tile(false, pl.splits_prefix, pl.splits_many);
+    if (pl.few) stream_part(false, pl.splits_prefix, pl.splits_few, pl.few_groups);
+    if (e == cudaSuccess && parts.n) {
+        PagedAttnParams f = p;
+        f.part_o = part_o;
+        f.part_lse = part_lse;
+        e = launch_paged_stream(f, parts, stream);
+    }
     if (e == cudaSuccess && pl.slots) {
         auto slots = [&](int splits) { return pl.splits_prefix || splits > 1 ? pl.splits_prefix + splits : 0; };
         p.part_o = part_o;

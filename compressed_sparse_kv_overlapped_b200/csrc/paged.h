@@ -50,7 +50,6 @@ struct PagedAttnParams {
     // this launch writes the partial slot part_base + s: part_o [slot][rows][H][d] (normalized, fp32),
     // part_lse [slot][rows][H] (base 2; -inf: an empty partial, its part_o is not written)
     int splits, part_base;
-    int split_groups;   // stream kernel: 16-key groups of a split (split s: [s, s + 1) times these, as far as there are)
     float* part_o;
     float* part_lse;
     int* status;
@@ -58,7 +57,21 @@ struct PagedAttnParams {
 };
 
 // Few query rows per key (decode): mma.sync tiles of 16 or 32 rows, each warp streaming its own keys.
-cudaError_t launch_paged_stream(const PagedAttnParams& p, cudaStream_t stream, bool pdl = false);
+// One launch takes up to two parts, the rows of all sequences on the prefix and each sequence's own keys;
+// these fields stand in the place of PagedAttnParams'.
+struct PagedStreamPart {
+    int prefix_mode, key_begin;
+    int splits, part_base;
+    int split_groups;   // 16-key groups of a split (split s: [s, s + 1) times these, as far as there are)
+    int row_tiles;      // (filled in by the launch)
+    bool partial;       // writes partials
+};
+struct PagedStreamParts {
+    PagedStreamPart part[2];
+    int n;
+    unsigned blocks0;   // blocks of part 0 (filled in by the launch)
+};
+cudaError_t launch_paged_stream(const PagedAttnParams& p, PagedStreamParts parts, cudaStream_t stream);
 // Many query rows per key: tcgen05 tiles of 128 rows.
 cudaError_t launch_paged_tile(const PagedAttnParams& p, cudaStream_t stream);
 // Tensor maps of the pools: boxes of 16 slots x 64 channels of one head and page, 128-byte swizzle.

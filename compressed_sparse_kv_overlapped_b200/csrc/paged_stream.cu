@@ -79,20 +79,35 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return pack_bf16x2(lo, hi);
 }
 
-// grid: x = ((b * row_tiles + row tile) * splits + split) * H_kv + key head
+// grid: for each part, x = ((b * row_tiles + row tile) * splits + split) * H_kv + key head
 template <int D, int MT, bool F16>
 __global__ void __launch_bounds__(kThreads)
-    paged_stream_kernel(const __grid_constant__ StreamMaps maps, const __grid_constant__ PagedAttnParams p, int row_tiles) {
+    paged_stream_kernel(const __grid_constant__ StreamMaps maps, const __grid_constant__ PagedAttnParams params,
+                        const __grid_constant__ PagedStreamParts parts) {
     using C = StreamCfg<D, MT>;
     extern __shared__ __align__(1024) unsigned char smem[];
     grid_dep_launch();
-    const csa_kv_cache& kv = p.kv;
+    unsigned u = blockIdx.x;
+    const bool second = u >= parts.blocks0;
+    if (second) u -= parts.blocks0;
+    const PagedStreamPart& part = parts.part[second ? 1 : 0];
+    PagedAttnParams p = params;
+    p.prefix_mode = part.prefix_mode;
+    p.key_begin = part.key_begin;
+    p.splits = part.splits;
+    p.part_base = part.part_base;
+    if (!part.partial) p.part_o = nullptr;
+    const int row_tiles = part.row_tiles, split_groups = part.split_groups;
+    const csa_kv_cache& kv = params.kv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {  // (fetched while the tables are read)
+        tma_prefetch_map(&maps.k);
+        tma_prefetch_map(&maps.v);
+    }
     if (smem_u32(smem) & 1023u) {  // (the swizzled boxes need it; the launch gives it)
         if (threadIdx.x == 0) report(p.status, CSA_ERR_CUDA);
         return;
     }
-    unsigned u = blockIdx.x;
     const int hk = (int)(u % (unsigned)kv.H_kv);
     u /= (unsigned)kv.H_kv;
     const int split = (int)(u % (unsigned)p.splits);
@@ -126,9 +141,9 @@ __global__ void __launch_bounds__(kThreads)
     // 16-key groups: those of the first tokens, then those of the window from lo rounded down
     const int n_first = (span.s1 + 15) >> 4, win0 = span.lo & ~15;
     const int n_groups = n_first + (span.hi > span.lo ? (span.hi - win0 + 15) >> 4 : 0);
-    const int g_begin = split * p.split_groups < n_groups ? split * p.split_groups : n_groups;
+    const int g_begin = split * split_groups < n_groups ? split * split_groups : n_groups;
     // (the last split takes the rest, should a sequence be longer than the host's bound)
-    const int g_end = split + 1 < p.splits && g_begin + p.split_groups < n_groups ? g_begin + p.split_groups : n_groups;
+    const int g_end = split + 1 < p.splits && g_begin + split_groups < n_groups ? g_begin + split_groups : n_groups;
     const int my = g_end - g_begin > warp ? (g_end - g_begin - warp + kWarps - 1) / kWarps : 0;
     if (g_begin == g_end && p.part_o) {  // nothing in this split: empty partials
         if ((int)threadIdx.x < R) {
@@ -442,14 +457,14 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
 }
 
 // Query rows of one key head, at most.
-int64_t most_rows(const PagedAttnParams& p) {
+int64_t most_rows(const PagedAttnParams& p, const PagedStreamPart& part) {
     const int64_t G = p.kv.H / p.kv.H_kv;
-    if (p.prefix_mode) return p.rows * G;
+    if (part.prefix_mode) return p.rows * G;
     return p.max_n * G < p.few_rows ? p.max_n * G : p.few_rows;
 }
 
 template <int D, int MT, bool F16>
-cudaError_t launch_stream(const PagedAttnParams& p, cudaStream_t stream, bool pdl) {
+cudaError_t launch_stream(const PagedAttnParams& p, PagedStreamParts& parts, cudaStream_t stream) {
     using C = StreamCfg<D, MT>;
     static PerDeviceOnce once;
     cudaError_t e = once.run([] {
@@ -457,33 +472,42 @@ cudaError_t launch_stream(const PagedAttnParams& p, cudaStream_t stream, bool pd
                                     C::kTotal);
     });
     if (e != cudaSuccess) return e;
-    const int64_t row_tiles = (most_rows(p) + C::kRows - 1) / C::kRows;
-    const int64_t grid = (p.prefix_mode ? 1 : p.kv.B) * row_tiles * p.kv.H_kv * p.splits;
-    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    int64_t grid = 0;
+    for (int i = 0; i < parts.n; ++i) {
+        PagedStreamPart& part = parts.part[i];
+        const int64_t row_tiles = (most_rows(p, part) + C::kRows - 1) / C::kRows;
+        part.row_tiles = (int)row_tiles;
+        grid += (part.prefix_mode ? 1 : p.kv.B) * row_tiles * p.kv.H_kv * part.splits;
+        if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        if (i == 0) parts.blocks0 = (unsigned)grid;
+    }
     StreamMaps maps;
     if ((e = paged_kv_maps(p.kv, &maps.k, &maps.v)) != cudaSuccess) return e;
     return launch_kernel(paged_stream_kernel<D, MT, F16>, dim3((unsigned)grid), dim3(kThreads), C::kTotal, stream,
-                         pdl, maps, p, (int)row_tiles);
+                         false, maps, p, parts);
 }
 
 template <int D>
-cudaError_t launch_stream_d(const PagedAttnParams& p, cudaStream_t stream, bool pdl) {
+cudaError_t launch_stream_d(const PagedAttnParams& p, PagedStreamParts& parts, cudaStream_t stream) {
     const bool f16 = p.kv.type == CSA_KV_F16;
-    if (most_rows(p) <= 16)
-        return f16 ? launch_stream<D, 1, true>(p, stream, pdl) : launch_stream<D, 1, false>(p, stream, pdl);
-    return f16 ? launch_stream<D, 2, true>(p, stream, pdl) : launch_stream<D, 2, false>(p, stream, pdl);
+    int64_t rows = 0;
+    for (int i = 0; i < parts.n; ++i) rows = most_rows(p, parts.part[i]) > rows ? most_rows(p, parts.part[i]) : rows;
+    if (rows <= 16) return f16 ? launch_stream<D, 1, true>(p, parts, stream) : launch_stream<D, 1, false>(p, parts, stream);
+    return f16 ? launch_stream<D, 2, true>(p, parts, stream) : launch_stream<D, 2, false>(p, parts, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_stream(const PagedAttnParams& p, cudaStream_t stream, bool pdl) {
-    return p.kv.d == 128 ? launch_stream_d<128>(p, stream, pdl) : launch_stream_d<64>(p, stream, pdl);
+cudaError_t launch_paged_stream(const PagedAttnParams& p, PagedStreamParts parts, cudaStream_t stream) {
+    return p.kv.d == 128 ? launch_stream_d<128>(p, parts, stream) : launch_stream_d<64>(p, parts, stream);
 }
 
 cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots_few, int slots_many, cudaStream_t stream,
                                  bool pdl) {
     const int heads = kCombineThreads / (p.kv.d / 4);
-    const int64_t blocks = ((int64_t)p.max_n * p.kv.H + heads - 1) / heads;
+    // rows of a sequence that has partials
+    const int64_t few = p.few_rows / (p.kv.H / p.kv.H_kv), n = slots_many || p.max_n < few ? p.max_n : few;
+    const int64_t blocks = (n * p.kv.H + heads - 1) / heads;
     const int64_t grid = blocks * p.kv.B;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const bool f16 = p.kv.type == CSA_KV_F16;
