@@ -122,10 +122,11 @@ int tile_splits(int64_t items, int64_t keys, int sms) {
 // ones leave little idle; a block never has more than kMostKeys keys, lest one long sequence outlast the
 // rest of its batch.
 int stream_splits(int64_t items, int64_t keys, int sms, int* groups) {
-    constexpr int64_t kWaves = 4, kLeastKeys = 256, kMostKeys = 8192, kMostSplits = 256;
+    constexpr int64_t kWaves = 2, kMostKeys = 8192, kMostSplits = 256;
     const int64_t places = 2 * (int64_t)sms;
+    const int64_t least = items * (keys / 128) <= places ? 128 : 256;
     int64_t s = items > 0 && items < places ? (kWaves * places + items - 1) / items : 1;
-    if (s > keys / kLeastKeys) s = keys / kLeastKeys;
+    if (s > keys / least) s = keys / least;
     if (s < (keys + kMostKeys - 1) / kMostKeys) s = (keys + kMostKeys - 1) / kMostKeys;
     if (s > kMostSplits) s = kMostSplits;
     if (s < 1) s = 1;
@@ -209,7 +210,7 @@ int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaS
     int fault = 0;
     debug_fault_state(&fault, &p.wait_ns);
     // the rows' parts: partials from slot `base` on, or directly into out when they are the only ones
-    auto tile = [&](bool prefix, int base, int splits) {
+    auto tile = [&](bool prefix, int base, int splits, bool pdl) {
         PagedAttnParams f = p;
         f.prefix_mode = prefix ? 1 : 0;
         if (prefix) f.key_begin = 0;
@@ -219,7 +220,7 @@ int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaS
             f.part_o = part_o;
             f.part_lse = part_lse;
         }
-        return launch_paged_tile(f, stream);
+        return launch_paged_tile(f, stream, pdl);
     };
     cudaError_t e = cudaSuccess;
     PagedStreamParts parts{};
@@ -227,18 +228,20 @@ int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaS
         parts.part[parts.n++] = PagedStreamPart{prefix ? 1 : 0, prefix ? 0 : p.key_begin, splits, base, groups, 0,
                                                 pl.splits_prefix || splits > 1};
     };
-    if (pl.splits_prefix) {
-        if (pl.prefix_tile) e = tile(true, 0, pl.splits_prefix);
-        else stream_part(true, 0, pl.splits_prefix, pl.prefix_groups);
-    }
-    if (e == cudaSuccess && pl.many) e = tile(false, pl.splits_prefix, pl.splits_many);
+    if (pl.splits_prefix && !pl.prefix_tile) stream_part(true, 0, pl.splits_prefix, pl.prefix_groups);
     if (pl.few) stream_part(false, pl.splits_prefix, pl.splits_few, pl.few_groups);
-    if (e == cudaSuccess && parts.n) {
+    // the first launch starts when all work before it is done; the others, on the same inputs and with
+    // partials and rows of their own, may overlap it
+    int launched = 0;
+    if (parts.n) {
         PagedAttnParams f = p;
         f.part_o = part_o;
         f.part_lse = part_lse;
         e = launch_paged_stream(f, parts, stream);
+        ++launched;
     }
+    if (e == cudaSuccess && pl.prefix_tile) e = tile(true, 0, pl.splits_prefix, launched++ > 0);
+    if (e == cudaSuccess && pl.many) e = tile(false, pl.splits_prefix, pl.splits_many, launched++ > 0);
     if (e == cudaSuccess && pl.slots) {
         auto slots = [&](int splits) { return pl.splits_prefix || splits > 1 ? pl.splits_prefix + splits : 0; };
         p.part_o = part_o;

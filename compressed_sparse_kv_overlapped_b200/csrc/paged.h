@@ -72,8 +72,9 @@ struct PagedStreamParts {
     unsigned blocks0;   // blocks of part 0 (filled in by the launch)
 };
 cudaError_t launch_paged_stream(const PagedAttnParams& p, PagedStreamParts parts, cudaStream_t stream);
-// Many query rows per key: tcgen05 tiles of 128 rows.
-cudaError_t launch_paged_tile(const PagedAttnParams& p, cudaStream_t stream);
+// Many query rows per key: tcgen05 tiles of 128 rows.  pdl: it may start before the launch in front of it,
+// one of the same call, ends (it ends after it).
+cudaError_t launch_paged_tile(const PagedAttnParams& p, cudaStream_t stream, bool pdl);
 // Tensor maps of the pools: boxes of 16 slots x 64 channels of one head and page, 128-byte swizzle.
 cudaError_t paged_kv_maps(const csa_kv_cache& kv, CUtensorMap* k, CUtensorMap* v);
 // Merge of the partial slots of each (row, head) into out / lse: slots_few of a sequence with few rows,

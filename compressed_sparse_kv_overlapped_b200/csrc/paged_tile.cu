@@ -712,19 +712,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive(bar);
         };
-        const int rt = r / g.G;
+        const int rt = r / g.G, rt_first = (warp & 3) * 32 / g.G, rt_last = ((warp & 3) * 32 + 31) / g.G;
         const float sc = p.scale_log2;
         uint32_t nb = 0, nt = 0;
         bool ok = true;
         for (int k = 0; ok && next_work(k); ++k) {
             const int T = w.t1 - w.t0;
             if (T == 0 || w.ntok <= q * g.tpt) continue;
-            const int p_first = w.p0 + q * g.tpt, p_last = w.p0 + (w.ntok < (q + 1) * g.tpt ? w.ntok : (q + 1) * g.tpt) - 1;
-            const int pos = p_first + rt;
+            // positions of the warp's rows (those of rows behind the last token are not looked at)
+            const int p_end = w.p0 + (w.ntok < (q + 1) * g.tpt ? w.ntok : (q + 1) * g.tpt) - 1;
+            const int p_first = w.p0 + q * g.tpt + rt_first;
+            const int p_last = w.p0 + q * g.tpt + rt_last < p_end ? w.p0 + q * g.tpt + rt_last : p_end;
+            const int pos = w.p0 + q * g.tpt + rt;
             const int wb = 16 * w.n_first - w.win0;  // index in the list of groups of a window token
             const int up = pos + 1 < w.hi ? pos + 1 : w.hi;
             const int low = pos - p.W + 1 > w.lo ? pos - p.W + 1 : w.lo;
             const int first_up = p.S < up ? p.S : up;
+            // tokens that some row of the warp sees: of the window [any_low, any_up), of the first tokens
+            // below any_first
+            const int any_up = p_last + 1 < w.hi ? p_last + 1 : w.hi;
+            const int any_low = p_first - p.W + 1 > w.lo ? p_first - p.W + 1 : w.lo;
+            const int any_first = p.S < any_up ? p.S : any_up;
             const int all_up = p_first + 1 < w.hi ? p_first + 1 : w.hi;  // tokens every row sees, but for the window
             const int width = 16 * w.gw;
             float m = -INFINITY;
@@ -738,18 +746,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 4; ++c)
                     if (c * 32 < width) tmem_ld32(ts + c * 32, s + c * 32);
                 tmem_ld_wait();
-                const bool wide = width == kTile;
-                const int i0 = (w.t0 + t) * width, tok0 = i0 - wb;
-                const bool whole = i0 + width <= w.s1 ||
-                                   (i0 >= 16 * w.n_first && tok0 >= w.lo && tok0 + width <= all_up &&
-                                    (tok0 > p_last - p.W || tok0 + width <= p.S));
-                if (!whole) {
+                const int i0 = (w.t0 + t) * width;
+                // a chunk of 32 keys is one that no row of the warp sees, that all see, or one to mask
+                uint32_t dead = 0, part = 0;
+                {
+                    const int tok0 = i0 - wb;
+                    const bool whole = width == kTile &&
+                                       (i0 + kTile <= w.s1 ||
+                                        (i0 >= 16 * w.n_first && tok0 >= w.lo && tok0 + kTile <= all_up &&
+                                         (tok0 > p_last - p.W || tok0 + kTile <= p.S)));
+                    if (!whole) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            const int x = i0 + c * 32, tok = x - wb;
+                            const bool some = x < w.s1 || (tok + 32 > any_low && tok < any_up) ||
+                                              (tok + 32 > w.lo && tok < any_first);
+                            const bool all = x + 32 <= w.s1 ||
+                                             (x >= 16 * w.n_first && tok >= w.lo && tok + 32 <= all_up &&
+                                              (tok > p_last - p.W || tok + 32 <= p.S));
+                            if (c * 32 >= width || !some) dead |= 1u << c;
+                            else if (!all) part |= 1u << c;
+                        }
+                    }
+                }
+                const bool plain = (dead | part) == 0;
+                if (!plain) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const int base = i0 + c * 32;
-                        const uint32_t see = bits32(0, w.s1, base) | bits32(wb + low, wb + up, base) |
-                                             bits32(wb + w.lo, wb + first_up, base);
-                        if (c * 32 < width && __any_sync(0xffffffffu, see != 0xffffffffu)) {
+                        if ((part >> c) & 1u) {
+                            const int base = i0 + c * 32;
+                            const uint32_t see = bits32(0, w.s1, base) | bits32(wb + low, wb + up, base) |
+                                                 bits32(wb + w.lo, wb + first_up, base);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (!((see >> i) & 1u)) s[c * 32 + i] = 0xff800000u;  // -inf
@@ -765,13 +792,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mx[e] = max3(mx[e], __uint_as_float(s[c * 32 + i + e]), __uint_as_float(s[c * 32 + i + e + 4]));
                     }
                 };
-                if (wide) {
+                if (plain) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) chunk_max(c);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (c * 32 < width) chunk_max(c);
+                        if (!((dead >> c) & 1u)) chunk_max(c);
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if (t == 0) {
@@ -818,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_st16(ts + c * 16, pk);
                 };
-                if (wide) {
+                if (plain) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         chunk_exp(c);
@@ -826,9 +853,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (c * 32 < width) chunk_exp(c);
-                    if (lane == 0) arrive(BAR(p_half, q));
+                    for (int c = 0; c < 4; ++c) {
+                        if (!((dead >> c) & 1u)) {
+                            chunk_exp(c);
+                        } else if (c * 32 < width) {
+                            uint32_t zero[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) zero[i] = 0u;
+                            tmem_st16(ts + c * 16, zero);
+                        }
+                    }
+                    stored(BAR(p_half, q));
                 }
                 stored(BAR(p_full, q));
             }
@@ -846,6 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             nt += T;
         }
     }
+    grid_dep_wait();  // (a launch that this one overlapped: whatever waits for this grid waits for that one too)
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag == 2) report(p.status, CSA_ERR_TIMEOUT);
@@ -855,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef BAR
 
 template <int D, bool F16>
-cudaError_t launch_tile(const PagedAttnParams& p, cudaStream_t stream) {
+cudaError_t launch_tile(const PagedAttnParams& p, cudaStream_t stream, bool pdl) {
     using C = TileCfg<D>;
     static PerDeviceOnce once;
     cudaError_t e = once.run([] {
@@ -876,7 +912,7 @@ cudaError_t launch_tile(const PagedAttnParams& p, cudaStream_t stream) {
     const int64_t most = (p.prefix_mode ? 1 : kv.B) * ((n + 2 * tpt - 1) / (2 * tpt)) * kv.H_kv * p.splits;
     if (most > 0x7fffffff) return cudaErrorInvalidConfiguration;
     return launch_kernel(paged_tile_kernel<D, F16>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), C::kTotal,
-                         stream, false, maps, p);
+                         stream, pdl, maps, p);
 }
 
 }  // namespace
@@ -892,10 +928,10 @@ cudaError_t paged_kv_maps(const csa_kv_cache& kv, CUtensorMap* k, CUtensorMap* v
     return e != cudaSuccess ? e : tensor_map_16bit(v, f16, kv.v_pages, 4, dims, strides, box);
 }
 
-cudaError_t launch_paged_tile(const PagedAttnParams& p, cudaStream_t stream) {
+cudaError_t launch_paged_tile(const PagedAttnParams& p, cudaStream_t stream, bool pdl) {
     const bool f16 = p.kv.type == CSA_KV_F16;
-    if (p.kv.d == 128) return f16 ? launch_tile<128, true>(p, stream) : launch_tile<128, false>(p, stream);
-    return f16 ? launch_tile<64, true>(p, stream) : launch_tile<64, false>(p, stream);
+    if (p.kv.d == 128) return f16 ? launch_tile<128, true>(p, stream, pdl) : launch_tile<128, false>(p, stream, pdl);
+    return f16 ? launch_tile<64, true>(p, stream, pdl) : launch_tile<64, false>(p, stream, pdl);
 }
 
 }  // namespace csa
