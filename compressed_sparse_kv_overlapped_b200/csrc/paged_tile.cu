@@ -127,6 +127,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -613,6 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t so = sbase + C::kOut + ew * C::kOutWarp;
         const unsigned char* sp = smem + C::kOut + ew * C::kOutWarp;
         const float2* ml = reinterpret_cast<const float2*>(smem + C::kMl);
+        constexpr int kRow = D * 2, kVec = kRow / 16, kRowsAt = 32 / kVec;
+        const int step_t = kRowsAt / g.G, step_h = kRowsAt % g.G;
         const uint32_t rcp = (65536u + g.G - 1) / g.G;  // r / G = r * rcp >> 16 for r < 128, G <= 64
         uint32_t nb0 = 0, nb1 = 0;
         bool ok = true;
@@ -644,8 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t to = tO(q) + ((uint32_t)er << 16);
                 // rows of D 16-bit values, or of D / 2 floats in two passes, through shared memory, so
                 // that whole rows go out as contiguous 16-byte vectors
-                constexpr int kRow = D * 2, kVec = kRow / 16, kRowsAt = 32 / kVec;
                 const int passes = p.part_o ? 2 : 1;
+                const uint64_t inv2 = pair2(inv, inv);
 #pragma unroll 1
                 for (int s = 0; s < passes; ++s) {
 #pragma unroll 1
@@ -654,14 +661,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t x[32];
                         tmem_ld32(to + c * 32, x);
                         tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float a, b;
+                            unpair2(mul2(pair2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), inv2), &a, &b);
+                            x[2 * i] = __float_as_uint(a);
+                            x[2 * i + 1] = __float_as_uint(b);
+                        }
                         if (passes == 1) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 uint32_t y[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    y[e] = pack16<F16>(__uint_as_float(x[8 * i + 2 * e]) * inv,
-                                                       __uint_as_float(x[8 * i + 2 * e + 1]) * inv);
+                                    y[e] = pack16<F16>(__uint_as_float(x[8 * i + 2 * e]), __uint_as_float(x[8 * i + 2 * e + 1]));
                                 st_shared_v4(so + lane * kRow + (((c * 4 + i) ^ (lane & 7)) << 4),
                                              make_uint4(y[0], y[1], y[2], y[3]));
                             }
@@ -669,10 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
                                 st_shared_v4(so + lane * kRow + ((((c % (D / 64)) * 8 + i) ^ (lane & 7)) << 4),
-                                             make_uint4(__float_as_uint(__uint_as_float(x[4 * i]) * inv),
-                                                        __float_as_uint(__uint_as_float(x[4 * i + 1]) * inv),
-                                                        __float_as_uint(__uint_as_float(x[4 * i + 2]) * inv),
-                                                        __float_as_uint(__uint_as_float(x[4 * i + 3]) * inv)));
+                                             make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
                         }
                     }
                     if (s == passes - 1) {
@@ -682,16 +692,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         __syncwarp();
                     }
+                    // the lane's vector of rows er + lane / kVec, + kRowsAt, ...: a step of kRowsAt heads, or on
+                    // to the next token
+                    const int v = lane % kVec;
+                    int lr = lane / kVec, tt = (int)((uint32_t)(er + lr) * rcp >> 16), h = er + lr - tt * g.G;
+                    const int64_t row_bytes = passes == 1 ? p.out_stride * 2 : (int64_t)kv.H * D * 4;
+                    const int head_bytes = passes == 1 ? D * 2 : D * 4;
+                    unsigned char* dst = passes == 1 ? reinterpret_cast<unsigned char*>(p.out) + v * 16
+                                                     : reinterpret_cast<unsigned char*>(p.part_o + part * kv.H * D + s * (D / 2)) + v * 16;
+                    dst += (row0 + tt) * row_bytes + (int64_t)(w.hk * g.G + h) * head_bytes;
+                    const int64_t step = step_t * row_bytes + step_h * head_bytes, wrap = row_bytes - g.G * head_bytes;
 #pragma unroll 4
-                    for (int i = 0; i < 32; i += kRowsAt) {
-                        const int lr = i + lane / kVec, v = lane % kVec, tr = er + lr;
+                    for (int i = 0; i < 32; i += kRowsAt, lr += kRowsAt) {
                         const uint4 y = *reinterpret_cast<const uint4*>(sp + lr * kRow + ((v ^ (lr & 7)) << 4));
-                        if (tr < nrow) {
-                            const int tt = (int)((uint32_t)tr * rcp >> 16), h = w.hk * g.G + (tr - tt * g.G);
-                            if (passes == 1)
-                                *reinterpret_cast<uint4*>(p.out + (row0 + tt) * p.out_stride + h * D + v * 8) = y;
-                            else
-                                *reinterpret_cast<uint4*>(p.part_o + ((part + row0 + tt) * kv.H + h) * D + s * (D / 2) + v * 4) = y;
+                        if (er + lr < nrow) *reinterpret_cast<uint4*>(dst) = y;
+                        dst += step;
+                        h += step_h;
+                        if (h >= g.G) {
+                            h -= g.G;
+                            dst += wrap;
                         }
                     }
                     __syncwarp();
@@ -712,27 +731,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive(bar);
         };
-        const int rt = r / g.G, rt_first = (warp & 3) * 32 / g.G, rt_last = ((warp & 3) * 32 + 31) / g.G;
+        const int rt = r / g.G;
         const float sc = p.scale_log2;
         uint32_t nb = 0, nt = 0;
         bool ok = true;
         for (int k = 0; ok && next_work(k); ++k) {
             const int T = w.t1 - w.t0;
             if (T == 0 || w.ntok <= q * g.tpt) continue;
-            // positions of the warp's rows (those of rows behind the last token are not looked at)
-            const int p_end = w.p0 + (w.ntok < (q + 1) * g.tpt ? w.ntok : (q + 1) * g.tpt) - 1;
-            const int p_first = w.p0 + q * g.tpt + rt_first;
-            const int p_last = w.p0 + q * g.tpt + rt_last < p_end ? w.p0 + q * g.tpt + rt_last : p_end;
-            const int pos = w.p0 + q * g.tpt + rt;
+            const int p_first = w.p0 + q * g.tpt, p_last = w.p0 + (w.ntok < (q + 1) * g.tpt ? w.ntok : (q + 1) * g.tpt) - 1;
+            const int pos = p_first + rt;
             const int wb = 16 * w.n_first - w.win0;  // index in the list of groups of a window token
             const int up = pos + 1 < w.hi ? pos + 1 : w.hi;
             const int low = pos - p.W + 1 > w.lo ? pos - p.W + 1 : w.lo;
             const int first_up = p.S < up ? p.S : up;
-            // tokens that some row of the warp sees: of the window [any_low, any_up), of the first tokens
-            // below any_first
-            const int any_up = p_last + 1 < w.hi ? p_last + 1 : w.hi;
-            const int any_low = p_first - p.W + 1 > w.lo ? p_first - p.W + 1 : w.lo;
-            const int any_first = p.S < any_up ? p.S : any_up;
             const int all_up = p_first + 1 < w.hi ? p_first + 1 : w.hi;  // tokens every row sees, but for the window
             const int width = 16 * w.gw;
             float m = -INFINITY;
@@ -746,37 +757,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 4; ++c)
                     if (c * 32 < width) tmem_ld32(ts + c * 32, s + c * 32);
                 tmem_ld_wait();
-                const int i0 = (w.t0 + t) * width;
-                // a chunk of 32 keys is one that no row of the warp sees, that all see, or one to mask
-                uint32_t dead = 0, part = 0;
-                {
-                    const int tok0 = i0 - wb;
-                    const bool whole = width == kTile &&
-                                       (i0 + kTile <= w.s1 ||
-                                        (i0 >= 16 * w.n_first && tok0 >= w.lo && tok0 + kTile <= all_up &&
-                                         (tok0 > p_last - p.W || tok0 + kTile <= p.S)));
-                    if (!whole) {
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            const int x = i0 + c * 32, tok = x - wb;
-                            const bool some = x < w.s1 || (tok + 32 > any_low && tok < any_up) ||
-                                              (tok + 32 > w.lo && tok < any_first);
-                            const bool all = x + 32 <= w.s1 ||
-                                             (x >= 16 * w.n_first && tok >= w.lo && tok + 32 <= all_up &&
-                                              (tok > p_last - p.W || tok + 32 <= p.S));
-                            if (c * 32 >= width || !some) dead |= 1u << c;
-                            else if (!all) part |= 1u << c;
-                        }
-                    }
-                }
-                const bool plain = (dead | part) == 0;
-                if (!plain) {
+                const bool wide = width == kTile;
+                const int i0 = (w.t0 + t) * width, tok0 = i0 - wb;
+                const bool whole = i0 + width <= w.s1 ||
+                                   (i0 >= 16 * w.n_first && tok0 >= w.lo && tok0 + width <= all_up &&
+                                    (tok0 > p_last - p.W || tok0 + width <= p.S));
+                if (!whole) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        if ((part >> c) & 1u) {
-                            const int base = i0 + c * 32;
-                            const uint32_t see = bits32(0, w.s1, base) | bits32(wb + low, wb + up, base) |
-                                                 bits32(wb + w.lo, wb + first_up, base);
+                        const int base = i0 + c * 32;
+                        const uint32_t see = bits32(0, w.s1, base) | bits32(wb + low, wb + up, base) |
+                                             bits32(wb + w.lo, wb + first_up, base);
+                        if (c * 32 < width && __any_sync(0xffffffffu, see != 0xffffffffu)) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (!((see >> i) & 1u)) s[c * 32 + i] = 0xff800000u;  // -inf
@@ -792,13 +784,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mx[e] = max3(mx[e], __uint_as_float(s[c * 32 + i + e]), __uint_as_float(s[c * 32 + i + e + 4]));
                     }
                 };
-                if (plain) {
+                if (wide) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) chunk_max(c);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (!((dead >> c) & 1u)) chunk_max(c);
+                        if (c * 32 < width) chunk_max(c);
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if (t == 0) {
@@ -845,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_st16(ts + c * 16, pk);
                 };
-                if (plain) {
+                if (wide) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         chunk_exp(c);
@@ -853,17 +845,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (!((dead >> c) & 1u)) {
-                            chunk_exp(c);
-                        } else if (c * 32 < width) {
-                            uint32_t zero[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) zero[i] = 0u;
-                            tmem_st16(ts + c * 16, zero);
-                        }
-                    }
-                    stored(BAR(p_half, q));
+                    for (int c = 0; c < 4; ++c)
+                        if (c * 32 < width) chunk_exp(c);
+                    if (lane == 0) arrive(BAR(p_half, q));
                 }
                 stored(BAR(p_full, q));
             }
