@@ -203,7 +203,8 @@ int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaS
     p.lse = a->lse;
     p.q_stride = a->q_stride;
     p.out_stride = a->out_stride;
-    p.few_rows = pl.many ? kFewRows : (int64_t)1 << 40;
+    // (without a stream launch the tile kernel takes every sequence, also one far shorter than max_n)
+    p.few_rows = !pl.many ? (int64_t)1 << 40 : pl.few ? kFewRows : 0;
     float* const part_o = static_cast<float*>(ws);
     float* const part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + pl.off_lse);
     if ((rc = device_status(&p.status))) return rc;

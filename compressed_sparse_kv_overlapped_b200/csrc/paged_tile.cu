@@ -444,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t uk = unit + 2 * t, uv = uk - 1;  // ring units of K(t) and V(t - 1)
                     const uint32_t ks = uk % C::kStages, vs = uv % C::kStages;
                     if (t > 0) ok = wait(BAR(kv_full, vs), uv / C::kStages) && wait(BAR(v_ready, vs), uv / C::kStages);
+                    if (ok && t < T) ok = wait(BAR(kv_full, ks), uk / C::kStages);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         if (!ok || q >= nq) break;
@@ -471,11 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (t == T) commit(BAR(o_full, q));
                         } else {
                             ok = wait(BAR(q_full, q), nb);
+                            if (!ok) break;
                         }
                         if (t < T) {
-                            if (ok && q == 0) ok = wait(BAR(kv_full, ks), uk / C::kStages);
-                            if (!ok) break;
-                            tc_fence_after();
                             const uint32_t qd = desc_lo(sbase + C::kQ + q * C::kOperand, 16);
                             const uint32_t kd = desc_lo(sbase + C::kKV + ks * C::kOperand, 16);
 #pragma unroll

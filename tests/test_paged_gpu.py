@@ -317,3 +317,97 @@ def test_results_do_not_change_from_call_to_call():
     for _ in range(3):
         w.attend()
         assert torch.equal(out, w.out) and torch.equal(lse, w.lse)
+
+
+# ------------------------------------------------------------------------------------- calls off the usual path
+
+@pytest.mark.parametrize("n,m", [(1, 300), (5, 40), (8, 8)])
+def test_one_sequence_far_below_the_bound_of_n(n, m):
+    """max_n only bounds: a captured call is made for the longest prompt and replayed for a short one."""
+    w = World(Case([(n, m)], H=8, H_kv=1, d=128, page=32, W=100, S=2))
+    w.max_n, w.max_len = 500, 2000
+    w.attend()
+    assert csa.csa_sync_status() == csa.CSA_OK
+    w.check()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (HF, 64)])
+@pytest.mark.parametrize("W,S,prefix", [(1 << 20, 0, 0), (3000, 40, 0), (0, 0, 700)])
+def test_single_tokens_and_prompts_in_one_call(dtype, d, W, S, prefix):
+    seqs = [(1, 9000), (300, 1100), (0, 800), (2, 5000), (130, 6000), (1, 701), (64, 900)]
+    run(Case(seqs, H=8, H_kv=1, d=d, page=64, dtype=dtype, W=W or 1 << 20, S=S, prefix=prefix, gap=1))
+
+
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_lengths_beyond_their_bound(prefix):
+    """max_len sizes the split of long rows; the keys come from the sequences' own lengths."""
+    for seqs in ([(1, 3000), (1, 700)], [(200, 3000), (1, 900)]):
+        w = World(Case(seqs, H=8, H_kv=2, d=128, page=64, W=1 << 20, prefix=prefix))
+        w.max_len = 1000
+        w.attend()
+        assert csa.csa_sync_status() == csa.CSA_OK
+        w.check()
+
+
+@pytest.mark.parametrize("prefix", [0, 1000])
+def test_captured_calls_share_a_workspace(prefix):
+    """Two graphs over one workspace, replayed in turn with changed queries, lengths and tables."""
+    cs = [Case([(1, 4000), (1, 1500), (140, 2500)], H=16, H_kv=2, d=128, page=64, W=1 << 20, prefix=prefix, seed=s)
+          for s in (3, 4)]
+    ws = [World(c) for c in cs]
+    args = [w.args() for w in ws]
+    space = max((w.kv.workspace(a) for w, a in zip(ws, args)), key=lambda t: t.numel())
+    graphs = []
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for w, a in zip(ws, args):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            w.attend(a, space)
+        graphs.append(g)
+    for _ in range(3):
+        for w, g in zip(ws, graphs):
+            w.q_full.copy_(w.q_full.roll(1, 0))
+            w.out_full.fill_(SENTINEL), w.lse.fill_(SENTINEL)
+            g.replay()
+    torch.cuda.synchronize()
+    assert csa.csa_sync_status() == csa.CSA_OK
+    for w in ws:
+        w.check()
+
+
+def test_pages_four_gigabytes_apart():
+    """Offsets in the pools pass 32 bits: pages 2^31 elements apart, appended to and attended."""
+    dev, H, H_kv, d, page, n, m = "cuda", 8, 2, 128, 16, 40, 40
+    step = 1 << 31
+    size = 2 * step + page * H_kv * d
+    pools = []
+    for _ in range(2):
+        flat = torch.empty(size, dtype=BF, device=dev)
+        pools.append(flat.as_strided((3, page, H_kv, d), (step, H_kv * d, d, 1)))
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=dev)
+    seqs = torch.tensor([[0, n, m]], dtype=torch.int64, device=dev)
+    kv = csa.PagedKV(*pools, table, seqs, H)
+    g = torch.Generator().manual_seed(9)
+    q, k, v = (torch.randn(n, h, d, generator=g).to(BF).to(dev) for h in (H, H_kv, H_kv))
+    kv.append(kv.append_args(k, v, max_n=n))
+    from tests.paged_harness import reference
+    for max_n in (n, 8):
+        rows = slice(n - max_n, n)
+        seqs.copy_(torch.tensor([[0, max_n, m]]))
+        out = torch.zeros(max_n, H, d, dtype=BF, device=dev)
+        a = kv.window_args(q[rows], out, W=1 << 20, max_n=max_n, max_len=m)
+        kv.window_attn(a, kv.workspace(a))
+        assert csa.csa_sync_status() == csa.CSA_OK
+        ref, _, tol, _ = reference(Case([(max_n, m)], H=H, H_kv=H_kv, d=d), q[rows].double().cpu(), k.double().cpu(),
+                                   v.double().cpu(), m - max_n, d ** -0.5)
+        assert ((out.double().cpu() - ref).abs() <= tol).all()
+
+
+def test_a_workspace_too_small_and_a_wrong_stream_are_refused():
+    w = World(Case([(1, 9001)], H=8, H_kv=1, d=128, page=64, W=1 << 20))
+    a = w.args()
+    ws = w.kv.workspace(a)
+    with pytest.raises(RuntimeError, match="workspace"):
+        w.kv.window_attn(a, ws[:ws.numel() - 256])
+    assert (w.out == SENTINEL).all()
