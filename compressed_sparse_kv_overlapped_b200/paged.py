@@ -19,7 +19,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import (CSA_KV_BF16, CSA_KV_F16, CSA_OP_PREFIX_ATTN, CSA_OP_WINDOW_ATTN, _check, _vp, csa_kv_append_args,
+from . import (CSA_KV_BF16, CSA_KV_F16, CSA_OP_PREFIX_ATTN, CSA_OP_WINDOW_ATTN, _check, csa_kv_append_args,
                csa_kv_attn_args, csa_kv_cache, csa_workspace_size, lib)
 
 
@@ -57,7 +57,11 @@ class PagedKV:
         kv.page_stride, kv.slot_stride, kv.head_stride = k_pages.stride()[:3]
         kv.k_pages, kv.v_pages = k_pages.data_ptr(), v_pages.data_ptr()
         kv.page_table, kv.seqs = page_table.data_ptr(), seqs.data_ptr()
+        # a call costs the host a few microseconds: what it needs is looked up here
         self._device_index = self.device.index
+        self._current_stream, self._current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        so = lib()
+        self._append_fn, self._window_fn, self._prefix_fn = so.csa_kv_append, so.csa_window_attn, so.csa_prefix_attn
 
     def _rows(self, t, heads, name):
         """Row stride of a [rows, heads, d] token array with contiguous heads."""
@@ -88,7 +92,7 @@ class PagedKV:
                   inv_freq.device == self.device, "inv_freq is a contiguous float32 vector on the cache's device")
             a.inv_freq, a.rot = inv_freq.data_ptr(), 2 * inv_freq.numel()
         a.interleaved = 1 if interleaved else 0
-        a._keep = (self, k, v, q, q_out, inv_freq)
+        a._keep, a._ref = (self, k, v, q, q_out, inv_freq), ctypes.byref(a)
         return a
 
     def _attn_args(self, q, out, max_n, max_len, lse, scale):
@@ -105,7 +109,7 @@ class PagedKV:
             _need(lse.dtype == torch.float32 and lse.shape == (q.shape[0], self.H) and lse.is_contiguous() and
                   lse.device == self.device, "lse is a contiguous float32 [rows, H] tensor on the cache's device")
             a.lse = lse.data_ptr()
-        a._keep = (self, q, out, lse)
+        a._keep, a._ref = (self, q, out, lse), ctypes.byref(a)
         return a
 
     def window_args(self, q, out, *, W, S=0, max_n, max_len=None, lse=None, scale=None) -> csa_kv_attn_args:
@@ -134,33 +138,30 @@ class PagedKV:
             n = 256
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
-    def _call(self, name, args, ws, stream):
-        import torch
-
+    def _call(self, name, fn, stream, *args):
         index = self._device_index
         if stream is None:
-            handle = torch.cuda.current_stream(index).cuda_stream
-        elif isinstance(stream, int):
-            handle = stream
-        else:
+            stream = self._current_stream(index)
+        elif not isinstance(stream, int):
             _need(stream.device == self.device, f"a stream of {stream.device} for a cache on {self.device}")
-            handle = stream.cuda_stream
-        fn = getattr(lib(), name)
-        a = (ctypes.byref(args), _vp(handle)) if name == "csa_kv_append" else \
-            (ctypes.byref(args), ws.data_ptr() if ws is not None else None, ws.nbytes if ws is not None else 0, _vp(handle))
-        if torch.cuda.current_device() == index:
-            rc = fn(*a)
+            stream = stream.cuda_stream
+        if self._current_device() == index:
+            rc = fn(*args, stream)
         else:
+            import torch
+
             with torch.cuda.device(index):
-                rc = fn(*a)
+                rc = fn(*args, stream)
         if rc:
             _check(rc, name)
 
     def append(self, args: csa_kv_append_args, stream=None) -> None:
-        self._call("csa_kv_append", args, None, stream)
+        self._call("csa_kv_append", self._append_fn, stream, args._ref)
 
     def window_attn(self, args: csa_kv_attn_args, ws, stream=None) -> None:
-        self._call("csa_window_attn", args, ws, stream)
+        ptr, size = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
+        self._call("csa_window_attn", self._window_fn, stream, args._ref, ptr, size)
 
     def prefix_attn(self, args: csa_kv_attn_args, ws, stream=None) -> None:
-        self._call("csa_prefix_attn", args, ws, stream)
+        ptr, size = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
+        self._call("csa_prefix_attn", self._prefix_fn, stream, args._ref, ptr, size)
