@@ -413,15 +413,17 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedAttnParams p, int slots_few, int slots_many,
                                                                 int blocks) {
     constexpr int kLanes = D / 4, kHeads = kCombineThreads / kLanes;
-    grid_dep_wait();
     const csa_kv_cache& kv = p.kv;
     const int b = (int)(blockIdx.x / (unsigned)blocks);
     csa_kv_seq seq;
-    if (!paged_seq(kv, b, p.rows, p.max_n, p.prefix_len, nullptr, false, &seq)) return;
+    bool live = paged_seq(kv, b, p.rows, p.max_n, p.prefix_len, nullptr, false, &seq);
     const int64_t f = (int64_t)(blockIdx.x % (unsigned)blocks) * kHeads + threadIdx.x / kLanes;
-    if (f >= seq.n * kv.H) return;
     const int slots = seq.n * (kv.H / kv.H_kv) <= p.few_rows ? slots_few : slots_many;
-    if (slots == 0) return;
+    live = live && f < seq.n * kv.H && slots > 0;
+    // (the tables above are older than the launches that wrote the partials; every block waits for these,
+    // so that this grid never ends before them)
+    grid_dep_wait();
+    if (!live) return;
     const int ln = threadIdx.x % kLanes, c = ln * 4;
     const int64_t at = seq.row * kv.H + f, step = p.rows * kv.H;
     // a head's lanes read the sums of kLanes slots at once and pass them round

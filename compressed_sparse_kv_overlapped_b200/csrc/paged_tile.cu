@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (the shuffle tells the compiler that a warp's threads take the same branches)
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const csa_kv_cache& kv = p.kv;
+    grid_dep_launch();
     if (sbase & 1023u) {  // (the swizzled layout needs it; the launch gives it)
         if (threadIdx.x == 0) report(p.status, CSA_ERR_CUDA);
         return;
