@@ -438,16 +438,23 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
     for (int base = 0; base < slots; base += kLanes) {
         const float mine = base + ln < slots ? fast_exp2(p.part_lse[at + (base + ln) * step] - mu) : 0.f;
         const int cnt = slots - base < kLanes ? slots - base : kLanes;
-#pragma unroll 8
-        for (int j = 0; j < cnt; ++j) {
-            const float w = __shfl_sync(mask, mine, j, kLanes);
-            if (w == 0.f) continue;  // (an empty partial has no output)
-            const float4 x = *reinterpret_cast<const float4*>(p.part_o + (at + (base + j) * step) * D + c);
-            sum += w;
-            acc.x = fmaf(x.x, w, acc.x);
-            acc.y = fmaf(x.y, w, acc.y);
-            acc.z = fmaf(x.z, w, acc.z);
-            acc.w = fmaf(x.w, w, acc.w);
+        for (int j0 = 0; j0 < cnt; j0 += 8) {  // eight loads in flight
+            float4 x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int slot = base + j0 + j < slots ? base + j0 + j : slots - 1;
+                x[j] = *reinterpret_cast<const float4*>(p.part_o + (at + slot * step) * D + c);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float w = __shfl_sync(mask, mine, j0 + j, kLanes);
+                if (w == 0.f) continue;  // (past the last, or an empty partial, whose output was not written)
+                sum += w;
+                acc.x = fmaf(x[j].x, w, acc.x);
+                acc.y = fmaf(x[j].y, w, acc.y);
+                acc.z = fmaf(x[j].z, w, acc.z);
+                acc.w = fmaf(x[j].w, w, acc.w);
+            }
         }
     }
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
