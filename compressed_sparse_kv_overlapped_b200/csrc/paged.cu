@@ -84,7 +84,10 @@ struct PagedPlan {
     size_t off_lse, total;
 };
 
-// Rows of one key head up to which the stream kernel is used.
+// Rows of one key head up to which the stream kernel is used.  It reads a block's keys once per 32 rows,
+// the tile kernel once per 256 but with at least a tile's time (2 us) per 128 keys: 128 rows on a prefix of
+// 8,192 take 39 us here through the tile kernel and 92 through the stream kernel; up to 64 rows, where
+// long rows are split over all SMs, the stream kernel's launch is the shorter one.
 constexpr int64_t kFewRows = 64;
 constexpr int64_t kFewPrefixRows = 64;  // the same for the rows of all sequences on the prefix
 
@@ -119,7 +122,9 @@ int tile_splits(int64_t items, int64_t keys, int sms) {
 // The stream kernel's cut: splits of `groups` 16-key groups each, for `items` blocks that see up to `keys`
 // keys.  Lengths are known on the device only, so a split is a fixed number of keys: a shorter sequence
 // has fewer.  Few blocks are cut until there are kWaves per resident place (two an SM), so that the last
-// ones leave little idle; a block never has more than kMostKeys keys, lest one long sequence outlast the
+// ones leave little idle (32 rows over 4,096 keys / five over 65,536: 111 / 297 us with one, 115 / 219 with
+// two, 119 / 224 with four, 125 / 242 with eight); splits have 256 keys, or 128 where all of them still
+// run at once (1,000 keys of two heads: 14 instead of 18 us); a block never has more than kMostKeys keys, lest one long sequence outlast the
 // rest of its batch.
 int stream_splits(int64_t items, int64_t keys, int sms, int* groups) {
     constexpr int64_t kWaves = 2, kMostKeys = 8192, kMostSplits = 256;

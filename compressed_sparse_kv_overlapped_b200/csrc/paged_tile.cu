@@ -3,14 +3,16 @@
 //
 // A block is one key head and up to two tiles of 128 query rows; row r of a tile is head r % G of the
 // group of token r / G, so all G heads of a token share each key that is loaded.  Its keys are the
-// 16-key groups of its visible runs (first tokens, then window), eight groups to a key tile:
+// 16-key groups of its visible runs (first tokens, then window), up to eight groups to a key tile (tiles
+// of equal width: twelve groups are two tiles of 96 keys, not of 128 and 64):
 //     S = Q K^T     (128 x 128, over d)      tcgen05, Q and K from shared memory, S in TMEM
 //     P = 2^(scale S - m)                    one thread per row, P back into the columns of its S
 //     O += P V      (128 x d, over 128 keys) tcgen05, P from TMEM, V from shared memory, O in TMEM
 // The reference m of a row is not its running maximum but a maximum that is moved (and O and the sum
 // rescaled) only when the true one passes it by 2^8: weights then reach 2^8 at most, far from either
 // type's range, and O is hardly ever touched between products.  One tile's softmax runs while the
-// tensor pipe works for the other tile.
+// tensor pipe works for the other tile; the product of the first 64 keys starts when their weights are
+// stored (8 % on causal prompts).
 //
 // A 16-key group never crosses a page, so it is one TMA box per 64 channels: a warp's lanes each look
 // up and issue one box.  A group behind the last and a page number out of range become a coordinate
@@ -24,6 +26,19 @@
 //
 // Warps: 0-3 / 4-7 softmax of tile 0 / 1, 8-11 epilogue, 12 MMA issuer, 13 key loader, 14 look-up of
 // the blocks and query loader, 15 zeroing of dead V rows.  Every wait is bounded and winds the CTA down.
+//
+// Measured (bf16, d = 128): causal prompts of 77 to 8,191 tokens, 32 heads on 8, 0.84 ms = 0.97 PFLOP/s
+// (0.59 of a cuBLAS GEMM); the tensor pipe is 53 % busy and issue slots 41 %.  Bound by the chain of one
+// tile: of its period of about 3,700 clocks the softmax of a row tile takes about 2,500 (512 clocks of
+// loads and maximum, the rest exponentials at 16 a clock and SM, shared with the other tile's) and the
+// products 1,000.  A prompt of 32,768 with a window of 128: 0.44 ms for 1.2 GB (0.42 of the copy rate),
+// two key tiles a block, so every latency of the chain shows.  Measured and not taken: a share of the
+// exponentials as a polynomial on the FMA pipe (5 % slower: that unit is no limit), two threads per row
+// (768 threads; 15 % slower on causal prompts, 3 % faster at d = 64), scores read twice from TMEM in
+// short loops (10 % slower with a window of 128), P handed over after 32 or 96 keys (1 % slower).
+// What helped most after the first form was short code: the roles share the instruction cache, and a
+// warp-uniform role index, 32-bit barrier addresses and products issued several per block of code took
+// causal prompts from 1.01 to 0.93 ms.
 #include <cstddef>
 
 #include "paged.h"
@@ -34,6 +49,10 @@ namespace csa {
 namespace {
 
 constexpr int kThreads = 512;
+// Registers of a thread: at launch, and of the softmax, epilogue and last four warps after the exchange
+// between them, which waits until they are there.
+constexpr int kRegs = 128, kRegsSoftmax = 192, kRegsEpilogue = 80, kRegsLast = 48;
+static_assert(256 * kRegsSoftmax + 128 * kRegsEpilogue + 128 * kRegsLast <= kThreads * kRegs, "registers of a block");
 constexpr int kTile = 128;             // query rows and keys of a tile
 constexpr int kBlk = kTile * 128;      // bytes of 128 rows x 64 channels
 constexpr int kWorks = 4;              // blocks looked up ahead
@@ -427,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLast));
         if (warp == 12) {
             // ---------------------------------------------------------------- MMA issuer
             constexpr uint32_t id_o = idesc_16<F16>(kTile, D, true);
@@ -613,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 8) {
         // -------------------------------------------------------------------- epilogue
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsEpilogue));
         const int ew = warp - 8, er = ew * 32;  // this warp's rows of a tile
         const uint32_t so = sbase + C::kOut + ew * C::kOutWarp;
         const unsigned char* sp = smem + C::kOut + ew * C::kOutWarp;
@@ -720,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // -------------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int q = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tS(q) + lanes, to = tO(q) + lanes;
@@ -879,6 +898,11 @@ cudaError_t launch_tile(const PagedAttnParams& p, cudaStream_t stream, bool pdl)
     using C = TileCfg<D>;
     static PerDeviceOnce once;
     cudaError_t e = once.run([] {
+        // (the exchange of registers would wait for ever in a block that starts with fewer than it counts on)
+        cudaFuncAttributes attr;
+        const cudaError_t err = cudaFuncGetAttributes(&attr, paged_tile_kernel<D, F16>);
+        if (err != cudaSuccess) return err;
+        if (attr.numRegs < kRegs) return cudaErrorInvalidConfiguration;
         return cudaFuncSetAttribute(paged_tile_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
     });
     if (e != cudaSuccess) return e;

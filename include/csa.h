@@ -412,6 +412,8 @@ typedef struct csa_kv_attn_args {
  * token t <= p with t > p - W or t < S.  W >= len is plain causal attention.  Any mix of single new
  * tokens, a few proposed ones, prompts and chunks of prompts.
  *   out = sum_t softmax_t(scale q . K_t) V_t,  lse = log sum_t exp(scale q . K_t).
+ * Tokens that some query of the call sees need finite values: a weight of zero does not take an infinity
+ * or a NaN in V out of the other queries of its sequence.
  * Scores, softmax statistics and sums are held in 32 bits; the weights are rounded to the cache's type
  * for the product with V, the output once at the end.  Workspace: CSA_OP_WINDOW_ATTN; calls that may
  * run at the same time (two streams, two graphs) need a workspace each. */
