@@ -80,8 +80,9 @@ struct PagedPlan {
     bool prefix_tile;
     int splits_prefix;           // 0: no prefix
     int few_groups, prefix_groups;  // 16-key groups of a split of the stream kernel
-    int slots;                   // partials per (row, head); 0: all written directly
-    size_t off_lse, total;
+    PagedMerge merge;            // partials, their pointers offsets into the workspace
+    bool any;                    // there are some
+    size_t total;
 };
 
 // Rows of one key head up to which the stream kernel is used.  It reads a block's keys once per 32 rows,
@@ -144,8 +145,7 @@ PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
     PagedPlan pl{};
     const int64_t G = a.kv.H / a.kv.H_kv, cap = a.kv.max_pages * a.kv.page_size, B = a.kv.B;
     const int64_t max_len = a.max_len < cap ? a.max_len : cap;
-    int64_t n = a.max_n < max_len ? a.max_n : max_len;
-    if (n > a.rows) n = a.rows;
+    const int64_t n = a.max_n < a.rows ? a.max_n : a.rows;  // (what the kernels bound a sequence's n by)
     const int64_t n_few = n * G > kFewRows ? kFewRows / G : n, tpb = 2 * (128 / G);
     const int sms = sm_count_or(148);
     auto stream_items = [&](int64_t seqs, int64_t rows) { return seqs * a.kv.H_kv * ((rows * G + 31) / 32); };
@@ -168,11 +168,26 @@ PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
                                ? tile_splits(a.kv.H_kv * ((a.rows + tpb - 1) / tpb), a.prefix_len, sms)
                                : stream_splits(stream_items(1, a.rows), a.prefix_len, sms, &pl.prefix_groups);
     }
-    const int most = pl.splits_few > pl.splits_many ? pl.splits_few : pl.splits_many;
-    pl.slots = pl.splits_prefix || most > 1 ? pl.splits_prefix + most : 0;
-    const size_t heads = (size_t)a.rows * a.kv.H * pl.slots;
-    pl.off_lse = align256(heads * a.kv.d * 4);
-    pl.total = pl.off_lse + align256(heads * 4);
+    // partials of the prefix for all rows; of a class of sequences where it is split or has a prefix, those of
+    // few rows by sequence (the rows of a prompt beside them need none)
+    auto partials = [&](int splits, int64_t rows, int64_t per_seq) {
+        PagedPartials q{};
+        q.rows = rows;
+        q.per_seq = (int)per_seq;
+        q.slots = splits;
+        return q;
+    };
+    if (pl.splits_prefix) pl.merge.prefix = partials(pl.splits_prefix, a.rows, 0);
+    if (pl.few && (pl.splits_prefix || pl.splits_few > 1)) pl.merge.few = partials(pl.splits_few, B * n_few, n_few);
+    if (pl.many && (pl.splits_prefix || pl.splits_many > 1)) pl.merge.many = partials(pl.splits_many, a.rows, 0);
+    for (PagedPartials* q : {&pl.merge.prefix, &pl.merge.few, &pl.merge.many}) {
+        const size_t heads = (size_t)q->rows * a.kv.H * q->slots;
+        pl.any = pl.any || q->slots;
+        q->o = reinterpret_cast<float*>(pl.total);
+        pl.total += align256(heads * a.kv.d * 4);
+        q->lse = reinterpret_cast<float*>(pl.total);
+        pl.total += align256(heads * 4);
+    }
     if (pl.total < 256) pl.total = 256;
     return pl;
 }
@@ -190,8 +205,8 @@ int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaS
     if (!stride_ok(a->q_stride, width) || !stride_ok(a->out_stride, width))
         return set_error(CSA_ERR_ARG, "q_stride = %lld, out_stride = %lld (multiples of 8, >= H d = %lld)",
                          (long long)a->q_stride, (long long)a->out_stride, (long long)width);
-    const PagedPlan pl = make_plan(*a, op);
-    if (pl.slots && (!ws || ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(ws) & 255u)))
+    PagedPlan pl = make_plan(*a, op);
+    if (pl.any && (!ws || ws_bytes < pl.total || (reinterpret_cast<uintptr_t>(ws) & 255u)))
         return set_error(CSA_ERR_ARG, "workspace: %zu bytes at a 256-byte aligned address needed, %zu given", pl.total,
                          ws ? ws_bytes : (size_t)0);
     PagedAttnParams p{};
@@ -210,50 +225,39 @@ int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaS
     p.out_stride = a->out_stride;
     // (without a stream launch the tile kernel takes every sequence, also one far shorter than max_n)
     p.few_rows = !pl.many ? (int64_t)1 << 40 : pl.few ? kFewRows : 0;
-    float* const part_o = static_cast<float*>(ws);
-    float* const part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + pl.off_lse);
+    for (PagedPartials* q : {&pl.merge.prefix, &pl.merge.few, &pl.merge.many}) {
+        unsigned char* const base = static_cast<unsigned char*>(ws);
+        q->o = q->slots ? reinterpret_cast<float*>(base + reinterpret_cast<size_t>(q->o)) : nullptr;
+        q->lse = q->slots ? reinterpret_cast<float*>(base + reinterpret_cast<size_t>(q->lse)) : nullptr;
+    }
     if ((rc = device_status(&p.status))) return rc;
     int fault = 0;
     debug_fault_state(&fault, &p.wait_ns);
-    // the rows' parts: partials from slot `base` on, or directly into out when they are the only ones
-    auto tile = [&](bool prefix, int base, int splits, bool pdl) {
+    auto tile = [&](bool prefix, int splits, const PagedPartials& partials, bool pdl) {
         PagedAttnParams f = p;
         f.prefix_mode = prefix ? 1 : 0;
         if (prefix) f.key_begin = 0;
         f.splits = splits;
-        f.part_base = base;
-        if (pl.splits_prefix || splits > 1) {
-            f.part_o = part_o;
-            f.part_lse = part_lse;
-        }
+        f.part = partials;
         return launch_paged_tile(f, stream, pdl);
     };
     cudaError_t e = cudaSuccess;
     PagedStreamParts parts{};
-    auto stream_part = [&](bool prefix, int base, int splits, int groups) {
-        parts.part[parts.n++] = PagedStreamPart{prefix ? 1 : 0, prefix ? 0 : p.key_begin, splits, base, groups, 0,
-                                                pl.splits_prefix || splits > 1};
+    auto stream_part = [&](bool prefix, int splits, int groups, const PagedPartials& partials) {
+        parts.part[parts.n++] = PagedStreamPart{prefix ? 1 : 0, prefix ? 0 : p.key_begin, splits, groups, 0, partials};
     };
-    if (pl.splits_prefix && !pl.prefix_tile) stream_part(true, 0, pl.splits_prefix, pl.prefix_groups);
-    if (pl.few) stream_part(false, pl.splits_prefix, pl.splits_few, pl.few_groups);
+    if (pl.splits_prefix && !pl.prefix_tile) stream_part(true, pl.splits_prefix, pl.prefix_groups, pl.merge.prefix);
+    if (pl.few) stream_part(false, pl.splits_few, pl.few_groups, pl.merge.few);
     // the first launch starts when all work before it is done; the others, on the same inputs and with
     // partials and rows of their own, may overlap it
     int launched = 0;
     if (parts.n) {
-        PagedAttnParams f = p;
-        f.part_o = part_o;
-        f.part_lse = part_lse;
-        e = launch_paged_stream(f, parts, stream);
+        e = launch_paged_stream(p, parts, stream);
         ++launched;
     }
-    if (e == cudaSuccess && pl.prefix_tile) e = tile(true, 0, pl.splits_prefix, launched++ > 0);
-    if (e == cudaSuccess && pl.many) e = tile(false, pl.splits_prefix, pl.splits_many, launched++ > 0);
-    if (e == cudaSuccess && pl.slots) {
-        auto slots = [&](int splits) { return pl.splits_prefix || splits > 1 ? pl.splits_prefix + splits : 0; };
-        p.part_o = part_o;
-        p.part_lse = part_lse;
-        e = launch_paged_combine(p, slots(pl.splits_few), slots(pl.splits_many), stream, true);
-    }
+    if (e == cudaSuccess && pl.prefix_tile) e = tile(true, pl.splits_prefix, pl.merge.prefix, launched++ > 0);
+    if (e == cudaSuccess && pl.many) e = tile(false, pl.splits_many, pl.merge.many, launched++ > 0);
+    if (e == cudaSuccess && pl.any) e = launch_paged_combine(p, pl.merge, stream, true);
     if (e != cudaSuccess) return set_error(CSA_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
     return CSA_OK;
 }

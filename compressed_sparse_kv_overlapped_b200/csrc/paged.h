@@ -26,6 +26,17 @@ struct PagedAppendParams {
 };
 cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t stream);
 
+// Partial results: o [slots][rows][H][d] (normalized, fp32), lse [slots][rows][H] (base 2; -inf: an empty
+// partial, its o is not written).  The row of token i of sequence b is that of the token arrays, or
+// b * per_seq + i where only sequences with up to per_seq tokens have partials.
+struct PagedPartials {
+    float* o;
+    float* lse;
+    int64_t rows;
+    int per_seq;
+    int slots;
+};
+
 // One launch of an attention kernel over keys [key_begin, key_end of the mode) of every query.
 struct PagedAttnParams {
     csa_kv_cache kv;
@@ -46,12 +57,10 @@ struct PagedAttnParams {
     // sequences with n G <= few_rows query rows per key head belong to the stream kernel, the others to
     // the tile kernel (without prefix_mode)
     int64_t few_rows;
-    // splits of the keys of a block: 1 with part_o = nullptr writes out / lse; otherwise split s of
-    // this launch writes the partial slot part_base + s: part_o [slot][rows][H][d] (normalized, fp32),
-    // part_lse [slot][rows][H] (base 2; -inf: an empty partial, its part_o is not written)
-    int splits, part_base;
-    float* part_o;
-    float* part_lse;
+    // splits of the keys of a block: split s writes slot s of the partials, or without any (part.o =
+    // nullptr, one split) out / lse
+    int splits;
+    PagedPartials part;
     int* status;
     uint64_t wait_ns;
 };
@@ -61,10 +70,10 @@ struct PagedAttnParams {
 // these fields stand in the place of PagedAttnParams'.
 struct PagedStreamPart {
     int prefix_mode, key_begin;
-    int splits, part_base;
+    int splits;
     int split_groups;   // 16-key groups of a split (split s: [s, s + 1) times these, as far as there are)
     int row_tiles;      // (filled in by the launch)
-    bool partial;       // writes partials
+    PagedPartials part;
 };
 struct PagedStreamParts {
     PagedStreamPart part[2];
@@ -77,9 +86,12 @@ cudaError_t launch_paged_stream(const PagedAttnParams& p, PagedStreamParts parts
 cudaError_t launch_paged_tile(const PagedAttnParams& p, cudaStream_t stream, bool pdl);
 // Tensor maps of the pools: boxes of 16 slots x 64 channels of one head and page, 128-byte swizzle.
 cudaError_t paged_kv_maps(const csa_kv_cache& kv, CUtensorMap* k, CUtensorMap* v);
-// Merge of the partial slots of each (row, head) into out / lse: slots_few of a sequence with few rows,
-// slots_many of another (0: written directly, left alone).
-cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots_few, int slots_many, cudaStream_t stream, bool pdl);
+// Merge of the partials of each (row, head) into out / lse: those of the prefix, and those of a sequence with
+// few rows or of another.  A sequence without any was written directly and is left alone.
+struct PagedMerge {
+    PagedPartials prefix, few, many;
+};
+cudaError_t launch_paged_combine(const PagedAttnParams& p, const PagedMerge& m, cudaStream_t stream, bool pdl);
 
 // ---------------------------------------------------------------------------------------------
 

@@ -101,8 +101,7 @@ __global__ void __launch_bounds__(kThreads)
     p.prefix_mode = part.prefix_mode;
     p.key_begin = part.key_begin;
     p.splits = part.splits;
-    p.part_base = part.part_base;
-    if (!part.partial) p.part_o = nullptr;
+    p.part = part.part;
     const int row_tiles = part.row_tiles, split_groups = part.split_groups;
     const csa_kv_cache& kv = params.kv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -151,10 +150,11 @@ __global__ void __launch_bounds__(kThreads)
     // (the last split takes the rest, should a sequence be longer than the host's bound)
     const int g_end = split + 1 < p.splits && g_begin + split_groups < n_groups ? g_begin + split_groups : n_groups;
     const int my = g_end - g_begin > warp ? (g_end - g_begin - warp + kWarps - 1) / kWarps : 0;
-    if (g_begin == g_end && p.part_o) {  // nothing in this split: empty partials
+    if (g_begin == g_end && p.part.o) {  // nothing in this split: empty partials
         if ((int)threadIdx.x < R) {
             const int64_t f = r0 + threadIdx.x, tok = f / G;
-            p.part_lse[((int64_t)(p.part_base + split) * p.rows + seq.row + tok) * kv.H + hk * G + (f - tok * G)] = -INFINITY;
+            const int64_t row = (int64_t)split * p.part.rows + (p.part.per_seq ? (int64_t)b * p.part.per_seq : seq.row) + tok;
+            p.part.lse[row * kv.H + hk * G + (f - tok * G)] = -INFINITY;
         }
         return;
     }
@@ -400,10 +400,11 @@ __global__ void __launch_bounds__(kThreads)
         const int64_t f = r0 + r, tok = f / G;
         const int64_t row = seq.row + tok;
         const int h = hk * G + (int)(f - tok * G);
-        if (p.part_o) {
-            const int64_t at = ((int64_t)(p.part_base + split) * p.rows + row) * kv.H + h;
-            *reinterpret_cast<float4*>(p.part_o + at * D + c) = acc;
-            if (c == 0) p.part_lse[at] = sum == 0.f ? -INFINITY : mu + log2f(sum);
+        if (p.part.o) {
+            const int64_t at =
+                ((int64_t)split * p.part.rows + (p.part.per_seq ? (int64_t)b * p.part.per_seq : seq.row) + tok) * kv.H + h;
+            *reinterpret_cast<float4*>(p.part.o + at * D + c) = acc;
+            if (c == 0) p.part.lse[at] = sum == 0.f ? -INFINITY : mu + log2f(sum);
         } else {
             *reinterpret_cast<uint2*>(p.out + row * p.out_stride + h * D + c) =
                 make_uint2(pack16<F16>(acc.x, acc.y), pack16<F16>(acc.z, acc.w));
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kThreads)
 // out = sum_s 2^(lse_s - lse) part_s, lse = log2 sum_s 2^(lse_s), over the slots of one (row, head):
 // D / 4 threads each take four channels.  grid: x = ((b * row blocks) + block)
 template <int D, bool F16>
-__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedAttnParams p, int slots_few, int slots_many,
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedAttnParams p, const PagedMerge m,
                                                                 int blocks) {
     constexpr int kLanes = D / 4, kHeads = kCombineThreads / kLanes;
     const csa_kv_cache& kv = p.kv;
@@ -425,32 +426,39 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
     csa_kv_seq seq;
     bool live = paged_seq(kv, b, p.rows, p.max_n, p.prefix_len, nullptr, false, &seq);
     const int64_t f = (int64_t)(blockIdx.x % (unsigned)blocks) * kHeads + threadIdx.x / kLanes;
-    const int slots = seq.n * (kv.H / kv.H_kv) <= p.few_rows ? slots_few : slots_many;
+    const PagedPartials& own = seq.n * (kv.H / kv.H_kv) <= p.few_rows ? m.few : m.many;
+    const int first = m.prefix.slots, slots = own.slots ? first + own.slots : 0;  // the prefix's slots come first
     live = live && f < seq.n * kv.H && slots > 0;
     // (the tables above are older than the launches that wrote the partials; every block waits for these,
     // so that this grid never ends before them)
     grid_dep_wait();
     if (!live) return;
     const int ln = threadIdx.x % kLanes, c = ln * 4;
-    const int64_t at = seq.row * kv.H + f, step = p.rows * kv.H;
+    const int64_t at = seq.row * kv.H + f;
+    const int64_t at_own = own.per_seq ? (int64_t)b * own.per_seq * kv.H + f : at;
+    auto sum_at = [&](int s) {
+        return s < first ? m.prefix.lse[at + s * m.prefix.rows * kv.H] : own.lse[at_own + (s - first) * own.rows * kv.H];
+    };
     // a head's lanes read the sums of kLanes slots at once and pass them round
     const unsigned mask = kLanes == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
     float top = -INFINITY;
-    for (int s = ln; s < slots; s += kLanes) top = fmaxf(top, p.part_lse[at + s * step]);
+    for (int s = ln; s < slots; s += kLanes) top = fmaxf(top, sum_at(s));
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, o, kLanes));
     const float mu = top == -INFINITY ? 0.f : top;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
     for (int base = 0; base < slots; base += kLanes) {
-        const float mine = base + ln < slots ? fast_exp2(p.part_lse[at + (base + ln) * step] - mu) : 0.f;
+        const float mine = base + ln < slots ? fast_exp2(sum_at(base + ln) - mu) : 0.f;
         const int cnt = slots - base < kLanes ? slots - base : kLanes;
         for (int j0 = 0; j0 < cnt; j0 += 8) {  // eight loads in flight
             float4 x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int slot = base + j0 + j < slots ? base + j0 + j : slots - 1;
-                x[j] = *reinterpret_cast<const float4*>(p.part_o + (at + slot * step) * D + c);
+                x[j] = *reinterpret_cast<const float4*>(
+                    (slot < first ? m.prefix.o + (at + slot * m.prefix.rows * kv.H) * D
+                                  : own.o + (at_own + (slot - first) * own.rows * kv.H) * D) + c);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -518,19 +526,17 @@ cudaError_t launch_paged_stream(const PagedAttnParams& p, PagedStreamParts parts
     return p.kv.d == 128 ? launch_stream_d<128>(p, parts, stream) : launch_stream_d<64>(p, parts, stream);
 }
 
-cudaError_t launch_paged_combine(const PagedAttnParams& p, int slots_few, int slots_many, cudaStream_t stream,
-                                 bool pdl) {
+cudaError_t launch_paged_combine(const PagedAttnParams& p, const PagedMerge& m, cudaStream_t stream, bool pdl) {
     const int heads = kCombineThreads / (p.kv.d / 4);
     // rows of a sequence that has partials
-    const int64_t few = p.few_rows / (p.kv.H / p.kv.H_kv), n = slots_many || p.max_n < few ? p.max_n : few;
+    const int64_t few = p.few_rows / (p.kv.H / p.kv.H_kv), n = m.many.slots || p.max_n < few ? p.max_n : few;
     const int64_t blocks = (n * p.kv.H + heads - 1) / heads;
     const int64_t grid = blocks * p.kv.B;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const bool f16 = p.kv.type == CSA_KV_F16;
     auto k = p.kv.d == 128 ? (f16 ? paged_combine_kernel<128, true> : paged_combine_kernel<128, false>)
                            : (f16 ? paged_combine_kernel<64, true> : paged_combine_kernel<64, false>);
-    return launch_kernel(k, dim3((unsigned)grid), dim3(kCombineThreads), 0, stream, pdl, p, slots_few, slots_many,
-                         (int)blocks);
+    return launch_kernel(k, dim3((unsigned)grid), dim3(kCombineThreads), 0, stream, pdl, p, m, (int)blocks);
 }
 
 }  // namespace csa

@@ -659,10 +659,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float lse = l == 0.f ? -INFINITY : m + log2f(l);  // base 2
                 const float inv = l != 0.f ? 1.f / l : 0.f;             // (a NaN sum stays NaN)
-                const int64_t part = (int64_t)(p.part_base + w.split) * p.rows;
+                const int64_t part = (int64_t)w.split * p.part.rows;  // (by row)
                 if (r < nrow) {
                     const int64_t at = (row0 + rt) * kv.H + w.hk * g.G + (r - rt * g.G);
-                    if (p.part_o) p.part_lse[part * kv.H + at] = lse;
+                    if (p.part.o) p.part.lse[part * kv.H + at] = lse;
                     else if (p.lse) p.lse[at] = lse * 0.69314718055994530942f;
                 }
                 if (w.t1 == w.t0) continue;
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t to = tO(q) + ((uint32_t)er << 16);
                 // rows of D 16-bit values, or of D / 2 floats in two passes, through shared memory, so
                 // that whole rows go out as contiguous 16-byte vectors
-                const int passes = p.part_o ? 2 : 1;
+                const int passes = p.part.o ? 2 : 1;
                 const uint64_t inv2 = pair2(inv, inv);
 #pragma unroll 1
                 for (int s = 0; s < passes; ++s) {
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int64_t row_bytes = passes == 1 ? p.out_stride * 2 : (int64_t)kv.H * D * 4;
                     const int head_bytes = passes == 1 ? D * 2 : D * 4;
                     unsigned char* dst = passes == 1 ? reinterpret_cast<unsigned char*>(p.out) + v * 16
-                                                     : reinterpret_cast<unsigned char*>(p.part_o + part * kv.H * D + s * (D / 2)) + v * 16;
+                                                     : reinterpret_cast<unsigned char*>(p.part.o + part * kv.H * D + s * (D / 2)) + v * 16;
                     dst += (row0 + tt) * row_bytes + (int64_t)(w.hk * g.G + h) * head_bytes;
                     const int64_t step = step_t * row_bytes + step_h * head_bytes, wrap = row_bytes - g.G * head_bytes;
 #pragma unroll 4

@@ -153,3 +153,12 @@ def test_visibility_of_the_reference():
     for i, p in enumerate(range(25, 30)):
         for t in range(30):
             assert bool(see[i, t]) == (t <= p and (t > p - 7 or t < 3))
+
+
+def test_workspace_of_prompts_beside_long_single_rows(lib):
+    """Rows of prompts are written directly: only the short rows of a mixed batch have partials."""
+    kv = cache(H=32, H_kv=8, d=128, B=3, page_size=64, max_pages=2048, page_stride=64 * 8 * 128, slot_stride=1024, head_stride=128)
+    a = attn_args(kv, rows=16384, max_n=8191, max_len=131072, W=1 << 40, q_stride=4096, out_stride=4096)
+    n = csa.csa_workspace_size(csa.CSA_OP_WINDOW_ATTN, a)
+    # at most 64 query rows of each key head of each sequence, at most 256 splits, 516 bytes a row
+    assert 256 < n <= 3 * 64 * 8 * 256 * 516 + 4096
