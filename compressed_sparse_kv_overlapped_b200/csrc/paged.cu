@@ -117,20 +117,38 @@ int tile_splits(int64_t items, int64_t keys, int sms) {
 
 // The stream kernel's cut: splits of `groups` 16-key groups each, for `items` blocks that see up to `keys`
 // keys.  Lengths are known on the device only, so a split is a fixed number of keys: a shorter sequence
-// has fewer.  Few blocks are cut until there are kWaves per resident place (two an SM), so that the last
-// ones leave little idle (32 rows over 4,096 keys / five over 65,536: 111 / 297 us with one, 115 / 219 with
-// two, 119 / 224 with four, 125 / 242 with eight); splits have 256 keys, or 128 where all of them still
-// run at once (1,000 keys of two heads: 14 instead of 18 us); a block never has more than kMostKeys keys, lest one long sequence outlast the
-// rest of its batch.
-int stream_splits(int64_t items, int64_t keys, int sms, int* groups) {
-    constexpr int64_t kWaves = 2, kMostKeys = 8192, kMostSplits = 256;
+// has fewer.  The number is the one with the least estimated time, in us: blocks run in rounds of two an
+// SM; a round takes its bytes at 6.4 TB/s, but no less than a block alone needs, 60 keys a us, and 1.5 to
+// start; a merge that would not be there otherwise costs 6, each split of a row 1 (0.25 beside a prefix).
+// Rows of 4,096 keys, 80 / 128 / 256 / 320 / 384 / 512 blocks: 48 / 71 / 108 / 142 / 157 / 191 us; cut for two
+// rounds whenever one is not full 60 / 83 / 120 / 181 / 184 / 191, uncut 78 / 78 / 106 / 182 / 184 / 188.
+// Where lengths may differ much (`even` is false: the window does not bound them) a split has 2,048 keys at
+// most, else 8,192, lest long sequences outlast the rest: causal rows of 1,000 to 8,000 keys, 512 blocks:
+// 212 us, uncut 246.  Long rows, where partials cost little, have two rounds of blocks whatever the estimate
+// says: five sequences of 40,000 to 131,072, window 65,536: 15 splits 214 us, 7 splits 234, 17 splits 246, 30
+// splits 225.  Never more than `most` splits.
+int stream_splits(int64_t items, int64_t keys, bool even, bool merged, int d, int sms, int64_t most, int* groups) {
+    constexpr int64_t kRagged = 2048, kEven = 8192;
+    constexpr double kBytesUs = 6.4e6, kKeysUs = 60.0, kStartUs = 1.5;
     const int64_t places = 2 * (int64_t)sms;
-    const int64_t least = items * (keys / 128) <= places ? 128 : 256;
-    int64_t s = items > 0 && items < places ? (kWaves * places + items - 1) / items : 1;
-    if (s > keys / least) s = keys / least;
-    if (s < (keys + kMostKeys - 1) / kMostKeys) s = (keys + kMostKeys - 1) / kMostKeys;
-    if (s > kMostSplits) s = kMostSplits;
-    if (s < 1) s = 1;
+    const int64_t least = items * (keys / 128) <= places ? 128 : 256;  // keys of a split
+    const int64_t longest = even ? kEven : kRagged, from = keys > longest ? (keys + longest - 1) / longest : 1;
+    int64_t s = from;
+    double best = 1e30;
+    for (int64_t i = from; i == from || (i <= 64 && i * least <= keys); ++i) {
+        const double share = (double)keys / (double)i, alone = share / kKeysUs, us = share * 4.0 * d / kBytesUs;
+        const int64_t full = items * i / places, rest = items * i % places;
+        double t = (double)full * (((double)places * us > alone ? (double)places * us : alone) + kStartUs);
+        if (rest) t += ((double)rest * us > alone ? (double)rest * us : alone) + kStartUs;
+        if (i > 1) t = 1.05 * t + (merged ? 0.25 * (double)i : 6.0 + (double)i);  // (a cut has to be worth it)
+        if (t < best) {
+            best = t;
+            s = i;
+        }
+    }
+    const int64_t two = items > 0 ? (2 * places + items - 1) / items : 1;  // splits for two rounds
+    if (items < places && keys >= two * kRagged) s = two;
+    if (s > most) s = most;
     const int64_t n = keys / 16 + 2;  // (both runs of keys may begin and end inside a group)
     *groups = (int)((n + s - 1) / s);
     return (int)((n + *groups - 1) / *groups);
@@ -151,17 +169,24 @@ PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
         const int64_t win = a.W < max_len ? a.W + q - 1 + (a.S < max_len ? a.S : max_len) : max_len;
         return win < max_len ? win : max_len;
     };
-    if (pl.few) pl.splits_few = stream_splits(stream_items(B, n_few), keys(n_few), sms, &pl.few_groups);
+    const bool prefix = op == CSA_OP_PREFIX_ATTN && a.prefix_len > 0;
+    if (pl.few) {
+        // (beside prompts most sequences may have none of these rows: no more than one round of blocks)
+        const int64_t items = stream_items(B, n_few), one_round = 2 * (int64_t)sms / items;
+        pl.splits_few = stream_splits(items, keys(n_few), op == CSA_OP_WINDOW_ATTN && a.W < max_len, prefix, a.kv.d, sms,
+                                      pl.many ? (one_round > 1 ? one_round : 1) : 256, &pl.few_groups);
+    }
     if (pl.many) {
         int64_t blocks = B * ((n + tpb - 1) / tpb);
         if (blocks > a.rows / tpb + B) blocks = a.rows / tpb + B;
         pl.splits_many = tile_splits(blocks * a.kv.H_kv, keys(tpb), sms);
     }
-    if (op == CSA_OP_PREFIX_ATTN && a.prefix_len > 0) {
+    if (prefix) {
         pl.prefix_tile = a.rows * G > kFewPrefixRows;
         pl.splits_prefix = pl.prefix_tile
                                ? tile_splits(a.kv.H_kv * ((a.rows + tpb - 1) / tpb), a.prefix_len, sms)
-                               : stream_splits(stream_items(1, a.rows), a.prefix_len, sms, &pl.prefix_groups);
+                               : stream_splits(stream_items(1, a.rows), a.prefix_len, true, true, a.kv.d, sms, 256,
+                                               &pl.prefix_groups);
     }
     // partials of the prefix for all rows; of a class of sequences where it is split or has a prefix, those of
     // few rows by sequence (the rows of a prompt beside them need none)

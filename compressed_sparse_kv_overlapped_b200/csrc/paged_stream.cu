@@ -22,8 +22,8 @@
 // 8 KiB at d = 128, 19 % busy) and tcgen05 would want 128 rows.
 //
 // Measured (d = 128, 8 key heads): five sequences with a window of 65,536, 1.24 GB in 193 us = 6.4 TB/s
-// (0.98 of the copy rate) and 210 us with the merge; 32 sequences with a window of 4,096, 542 MB in 98 us
-// = 5.5 TB/s, 103 us in all; one short row 5.8 us, a chain of latencies (tables, copy, merge of the
+// (0.98 of the copy rate) and 214 us with the merge; 32 sequences with a window of 4,096, 538 MB in 94 us
+// = 5.7 TB/s; one short row 5.8 us, a chain of latencies (tables, copy, merge of the
 // warps).  Copies by cp.async from eight warps of one block an SM took 324, 115 and 6.1 us: some 700
 // instructions a group, most of them addresses.
 #include "paged.h"
