@@ -411,3 +411,54 @@ def test_a_workspace_too_small_and_a_wrong_stream_are_refused():
     with pytest.raises(RuntimeError, match="workspace"):
         w.kv.window_attn(a, ws[:ws.numel() - 256])
     assert (w.out == SENTINEL).all()
+
+
+@pytest.mark.parametrize("n", [1, 90])
+def test_a_missing_page_counts_as_zeros(n):
+    """Keys and values of a page number out of range are zeros: score 0, no value (few rows and many)."""
+    c = Case([(n, 300), (n, 280)], H=8, H_kv=2, d=64, page=32, W=1 << 20)
+    w = World(c)
+    w.table[0, 2] = w.kp.shape[0] + 5
+    w.K[0][64:96] = 0
+    w.V[0][64:96] = 0
+    w.attend()
+    assert csa.csa_sync_status() == csa.CSA_ERR_INDEX
+    w.check()
+
+
+@pytest.mark.parametrize("n", [3, 90])
+def test_a_query_of_nan_stays_alone(n):
+    c = Case([(n, 300), (n, 280)], H=8, H_kv=2, d=128, page=32, W=100, S=3)
+    w = World(c)
+    w.q[1, 3] = math.nan
+    w.attend()
+    assert csa.csa_sync_status() == csa.CSA_OK
+    assert w.out[1, 3].isnan().all() and w.lse[1, 3].isnan()
+    w.q[1, 3] = 1.0
+    out, lse = w.out.clone(), w.lse.clone()
+    w.attend()
+    keep = torch.ones(w.rows, c.H, dtype=torch.bool, device="cuda")
+    keep[1, 3] = False
+    assert torch.equal(out[keep], w.out[keep]) and torch.equal(lse[keep], w.lse[keep])
+    w.check()
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_split_plans_of_many_batches(seed):
+    """Batches of many widths and lengths, so that every cut of long rows meets short and empty sequences."""
+    g = torch.Generator().manual_seed(50 + seed)
+    def pick(*a):
+        return a[int(torch.randint(len(a), (1,), generator=g))]
+    for _ in range(6):
+        B, top = pick(1, 3, 9, 40), pick(40, 700, 5000)
+        seqs = []
+        for _ in range(B):
+            n = pick(0, 1, 1, 1, 2, 4)
+            m = max(n, int(torch.randint(1, top + 1, (1,), generator=g)))
+            seqs.append((n, m))
+        seqs[0] = (1, top)
+        H_kv = pick(1, 2)
+        prefix = pick(0, 0, 17, 600)
+        seqs = [(n, m + prefix) for n, m in seqs]
+        run(Case(seqs, H=H_kv * pick(1, 3, 8), H_kv=H_kv, d=pick(64, 128), page=pick(16, 64), dtype=pick(BF, HF),
+                 W=1 << 20 if prefix else pick(30, 2000, 1 << 20), S=0 if prefix else pick(0, 5), prefix=prefix, seed=seed))
