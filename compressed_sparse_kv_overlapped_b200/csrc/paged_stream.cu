@@ -36,6 +36,12 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCombineThreads = 256;
+// What the weights are multiplied by for the product with V: fp16 has no normal numbers below 2^-14, and a row's
+// weights reach 1 at most.  With 2^15 one of 2^-29 of the largest is still normal and only those under 2^-40 are
+// lost; unscaled, 131,072 keys of 2^-25.2 behind one strong first token lose all of their 0.3 %.  bf16 has the
+// range of fp32.  A power of two: O is that much larger, without a further rounding, until it is divided by the sum.
+template <bool F16>
+constexpr float kWeightScale = F16 ? 32768.f : 1.f;
 
 struct StreamMaps {
     CUtensorMap k, v;
@@ -314,12 +320,14 @@ __global__ void __launch_bounds__(kThreads)
                 for (int c = 0; c < 4; ++c) {
                     const float w = fast_exp2(x[c] - mu);
                     l[ri] += w;
-                    s[t][c >> 1][2 * hh + (c & 1)] = w;
+                    s[t][c >> 1][2 * hh + (c & 1)] = w * kWeightScale<F16>;
                 }
             }
         }
-        // the weights, rounded to the cache's type, as the A operand of the product with V: the sum l
-        // keeps the unrounded ones (the rounding errors of the keys average out, at most half a step each)
+        // the weights, rounded to the cache's type, as the A operand of the product with V: at most half a step
+        // of each weight, 2^-40 of the row's largest for fp16's smallest ones; the sum l keeps the unrounded
+        // ones (the errors of the keys are independent, and one pass over V in the cache's type is what the
+        // tensor pipe takes)
         uint32_t pf[MT][4];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(kThreads)
             acc.z = fmaf(x.z, f, acc.z);
             acc.w = fmaf(x.w, f, acc.w);
         }
-        const float inv = sum != 0.f ? 1.f / sum : 0.f;  // (a NaN sum stays NaN)
+        const float inv = sum != 0.f ? 1.f / kWeightScale<F16> / sum : 0.f;  // (a NaN sum stays NaN)
         acc.x *= inv;
         acc.y *= inv;
         acc.z *= inv;

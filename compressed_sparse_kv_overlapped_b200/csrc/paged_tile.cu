@@ -6,7 +6,7 @@
 // 16-key groups of its visible runs (first tokens, then window), up to eight groups to a key tile (tiles
 // of equal width: twelve groups are two tiles of 96 keys, not of 128 and 64):
 //     S = Q K^T     (128 x 128, over d)      tcgen05, Q and K from shared memory, S in TMEM
-//     P = 2^(scale S - m)                    one thread per row, P back into the columns of its S
+//     P = 2^(scale S - m)                    one thread per row, P back into the columns of its S (fp16: 2^7 P)
 //     O += P V      (128 x d, over 128 keys) tcgen05, P from TMEM, V from shared memory, O in TMEM
 // The reference m of a row is not its running maximum but a maximum that is moved (and O and the sum
 // rescaled) only when the true one passes it by 2^8: weights then reach 2^8 at most, far from either
@@ -58,6 +58,12 @@ constexpr int kBlk = kTile * 128;      // bytes of 128 rows x 64 channels
 constexpr int kWorks = 4;              // blocks looked up ahead
 constexpr int kReaders = 15;           // warps that read them
 constexpr float kSlack = 8.f;          // base-2 units by which the maximum may pass its reference
+// Base-2 units added to the exponent of every weight: fp16 has no normal numbers below 2^-14, and weights reach
+// 2^(kSlack + kShift) = 2^15 at most.  So one of 2^-21 of the row's largest is still normal and only those under
+// 2^-32 are lost (2^-12 of the output with a million of them); unshifted, 131,072 keys of 2^-25.2 behind one strong
+// first token lose all of their 0.3 %.  bf16 has the range of fp32.  Sum and O grow alike.
+template <bool F16>
+constexpr float kShift = F16 ? 7.f : 0.f;
 
 struct TileMaps {
     CUtensorMap q, k, v;
@@ -228,6 +234,13 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
         return *reinterpret_cast<const uint32_t*>(&h);
     }
     return pack_bf16x2(lo, hi);
+}
+
+// The weight of a score s is 2^(s sc + weight_ref(m)): kShift - m sc, rounded so that no weight of a score up to m
+// passes 2^kShift, however large m is (0 while no key was seen, whose m is -inf).
+template <bool F16>
+__device__ __forceinline__ float weight_ref(float m, float sc) {
+    return m == -INFINITY ? 0.f : F16 ? __fmaf_rd(-m, sc, kShift<F16>) : -m * sc;
 }
 
 // Bits [from, to) of a 32-bit word that starts at `base`.
@@ -837,10 +850,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                const float neg = m == -INFINITY ? 0.f : -m * sc;
+                const float neg = weight_ref<F16>(m, sc);
                 const uint64_t sc2 = pair2(sc, sc), neg2 = pair2(neg, neg);
-                // the weights, rounded to the cache's type for the product with V: the sum keeps the
-                // unrounded ones (the rounding errors of the keys average out, half a step each at most)
+                // the weights, rounded to the cache's type for the product with V: at most half a step of each
+                // weight, 2^-32 of the row's reference for fp16's smallest ones; the sum keeps the unrounded
+                // ones (the errors of the keys are independent, and P in the cache's type is what the tensor
+                // pipe takes beside V)
                 auto chunk_exp = [&](int c) {
                     uint32_t pk[16];
 #pragma unroll
@@ -877,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float a, b, c, d;
             unpair2(l2[0], &a, &b);
             unpair2(l2[1], &c, &d);
-            ml[r] = make_float2(m == -INFINITY ? 0.f : m * sc, (a + b) + (c + d));
+            ml[r] = make_float2(-weight_ref<F16>(m, sc), (a + b) + (c + d));
             __syncwarp();
             if (lane == 0) arrive(BAR(ml_full, q));
             ++nb;

@@ -415,7 +415,8 @@ typedef struct csa_kv_attn_args {
  * Tokens that some query of the call sees need finite values: a weight of zero does not take an infinity
  * or a NaN in V out of the other queries of its sequence.
  * Scores, softmax statistics and sums are held in 32 bits; the weights are rounded to the cache's type
- * for the product with V, the output once at the end.  Workspace: CSA_OP_WINDOW_ATTN; calls that may
+ * for the product with V, relative to a scale at which fp16 keeps weights down to 2^-32 of a row's
+ * largest, the output once at the end.  Workspace: CSA_OP_WINDOW_ATTN; calls that may
  * run at the same time (two streams, two graphs) need a workspace each. */
 int csa_window_attn(const csa_kv_attn_args* args, void* ws, size_t ws_bytes, csa_stream_t stream);
 

@@ -1,0 +1,67 @@
+"""Cases of the paged key/value operators at the edges of their contracts: softmax weights far below a row's
+largest one."""
+import pytest
+import torch
+
+import compressed_sparse_kv_overlapped_b200 as csa
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+
+# Half a step of fp16's subnormal numbers, 2^-25, below the largest weight that the format holds at the kernel's
+# scale: 2^15 (one that a weight never passes) in the stream kernel, 2^7 in the tile kernel, whose largest weight
+# is 2^8 times that of the row's reference.
+LOST = {"stream": 2.0 ** -40, "tile": 2.0 ** -32}
+
+
+@pytest.mark.parametrize("dtype", [HF, BF])
+@pytest.mark.parametrize("kernel", ["stream", "tile"])
+@pytest.mark.parametrize("a,keys", [(2.1875, 65536), (2.1875, 8000), (1.640625, 4096)])
+def test_weights_far_below_the_first_tokens(dtype, kernel, a, keys):
+    """A first token that takes nearly all the weight and has no value, before a long uniform rest: each of the
+    rest's weights is 2^-25.2 (2^-18.9) of the first one's, their sum is the whole output.
+
+    Bound: relative h = eps / 2 for each rounding (weights, output), the fp32 errors of scores and sums, and an
+    absolute LOST for a weight below the type's normal numbers (bf16 has the range of fp32)."""
+    d, page, dev = 64, 256, "cuda"
+    if kernel == "tile":  # 80 blocks of 64 tokens: the keys are not split
+        B, H, H_kv, n, W, S = 1, 32, 8, 640, 1 << 20, 0
+    else:                 # 512 blocks of one row; the window and the first token
+        B, H, H_kv, n, W, S = 64, 8, 8, 1, min(keys, 8000), 1
+    m = keys + 1
+    pages = -(-m // page)
+    g = torch.Generator(device=dev).manual_seed(11)
+    kp = torch.zeros(pages, page, H_kv, d, dtype=dtype, device=dev)
+    vp = (1 + 0.25 * torch.randn(pages, page, H_kv, d, generator=g, device=dev)).to(dtype)
+    kp[0, 0], vp[0, 0] = a, 0
+    table = torch.arange(pages, dtype=torch.int32, device=dev).expand(B, -1).contiguous()
+    seqs = torch.tensor([[b * n, n, m] for b in range(B)], dtype=torch.int64, device=dev)
+    kv = csa.PagedKV(kp, vp, table, seqs, H)
+    q = torch.ones(B * n, H, d, dtype=dtype, device=dev)
+    out, lse = torch.zeros_like(q), torch.zeros(B * n, H, dtype=torch.float32, device=dev)
+    args = kv.window_args(q, out, W=W, S=S, max_n=n, max_len=m, lse=lse)
+    kv.window_attn(args, kv.workspace(args))
+    assert csa.csa_sync_status() == csa.CSA_OK
+
+    # in 64 bits: every key of the rest has score 0, the first one d a scale
+    first = torch.tensor(d * a * d ** -0.5, dtype=torch.float64, device=dev).exp()
+    V = vp.double().flatten(0, 1)
+    total = torch.cat((torch.zeros_like(V[:1]), V[1:m].cumsum(0)))        # [t]: V_1 + .. + V_t
+    mag = torch.cat((torch.zeros_like(V[:1]), V[1:m].abs().cumsum(0)))
+    pos = torch.arange(m - n, m, device=dev)
+    before = (pos - W).clamp(min=0)                                       # tokens 1 .. before are out of the window
+    rest = (pos - before).double()[:, None, None]
+    sums = first + rest
+    ref = (total[pos] - total[before]) / sums                             # [n, H_kv, d]
+    A = (mag[pos] - mag[before]) / sums
+    h, u = torch.finfo(dtype).eps / 2, 2.0 ** -24
+    rel = 2 * ((d + 8) * 2 * u * (d * a * d ** -0.5) + 2.0 ** -20) + 4 * (rest + 1) * u
+    lost = LOST[kernel] * rest * V.abs().max() if dtype == HF else 0.0
+    tol = (h + rel) * A + h * ref.abs() + lost + (2.0 ** -25 if dtype == HF else 0.0)
+    ref, tol = (x.repeat_interleave(H // H_kv, 1).repeat(B, 1, 1) for x in (ref, tol))
+    e = (out.double() - ref).abs()
+    assert (e <= tol).all(), f"off by {(e / tol).max():.1f} of the bound, {(e / ref.abs()).mean():.4f} of the value"
+    ref_lse = sums.log()[..., 0].repeat(B, 1)
+    assert ((lse.double() - ref_lse).abs() <= rel[..., 0].repeat(B, 1) + 2.0 ** -22 * ref_lse).all()
