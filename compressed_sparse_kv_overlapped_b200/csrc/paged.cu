@@ -251,8 +251,7 @@ int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaS
         q->lse = q->slots ? reinterpret_cast<float*>(base + reinterpret_cast<size_t>(q->lse)) : nullptr;
     }
     if ((rc = device_status(&p.status))) return rc;
-    int fault = 0;
-    debug_fault_state(&fault, &p.wait_ns);
+    debug_fault_state(&p.debug_fault, &p.wait_ns);
     auto tile = [&](bool prefix, int splits, const PagedPartials& partials, bool pdl) {
         PagedAttnParams f = p;
         f.prefix_mode = prefix ? 1 : 0;

@@ -63,6 +63,7 @@ struct PagedAttnParams {
     PagedPartials part;
     int* status;
     uint64_t wait_ns;
+    int debug_fault;    // 1 (tests of the bounded waits): the first wait for keys counts as run out
 };
 
 // Few query rows per key (decode): mma.sync tiles of 16 or 32 rows, each warp streaming its own keys.

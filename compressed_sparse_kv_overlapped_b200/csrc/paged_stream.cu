@@ -245,7 +245,9 @@ __global__ void __launch_bounds__(kThreads)
     int stage = 0;
     uint32_t phase = 0;
     int done = 0;
-    for (; done < my; ++done) {
+    const int run = p.debug_fault == 1 ? 0 : my;
+    if (run < my) report(p.status, CSA_ERR_TIMEOUT);
+    for (; done < run; ++done) {
         const int i = done;
         if (!__all_sync(0xffffffffu, mbar_wait(full + stage, phase, p.status, nullptr, p.wait_ns))) break;
         const uint32_t kb = ring + stage * (2 * C::kGroup), vb = kb + C::kGroup;
@@ -358,10 +360,10 @@ __global__ void __launch_bounds__(kThreads)
             phase ^= 1u;
         }
     }
-    // (after a wait that ran out: copies in flight land before the ring is used again)
-    for (int i = done + 1; done < my && i < my && i < done + C::kStages; ++i)
-        mbar_wait(full + i % C::kStages, (i / C::kStages) & 1, nullptr, nullptr, p.wait_ns);
-    __syncwarp();
+    // After a wait that ran out the copies in flight, that one's among them, land before the block ends: a wait of
+    // its own, whatever limit ran out.
+    for (int i = done; i < my && i < done + C::kStages; ++i)
+        mbar_wait(full + i % C::kStages, (i / C::kStages) & 1, nullptr, nullptr);
 
     // the warps' results meet: each in its own ring
     float* so = reinterpret_cast<float*>(smem + warp * C::kWarpBytes);
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(kThreads)
                     make_float2(o[t][j][2 * hh], o[t][j][2 * hh + 1]);
         }
     }
-    __syncthreads();
+    if (__syncthreads_or(done < my)) return;  // (reported; nothing is written)
     for (int i = threadIdx.x; i < R * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = (i % (D / 4)) * 4;
         float top = -INFINITY;

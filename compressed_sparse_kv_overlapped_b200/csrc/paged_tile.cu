@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dep_launch();
     if (sbase & 1023u) {  // (the swizzled layout needs it; the launch gives it)
         if (threadIdx.x == 0) report(p.status, CSA_ERR_CUDA);
+        grid_dep_wait();
         return;
     }
     TileGrid g;
@@ -416,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (misc[0] != 0) {  // (an allocation of every column starts at the first)
         if (threadIdx.x == 0) report(p.status, CSA_ERR_CUDA);
         if (warp == 12) tmem_dealloc(misc[0], 512);
+        grid_dep_wait();
         return;
     }
     g.total = counts[31] * kv.H_kv * p.splits;
@@ -441,11 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return __all_sync(0xffffffffu, done);
     };
-    auto drain = [&](uint32_t bar, uint32_t parity) {  // copies or products in flight, also after an abort
+    // Copies or products in flight: each role that issues some waits for its last ones before it ends, since any
+    // role may have given up on them.  A limit of its own, 2.1 seconds, whatever limit ran out.
+    auto drain = [&](uint32_t bar, uint32_t parity) {
         const uint32_t t0 = (uint32_t)clock();
 #pragma unroll 1
         while (!try_wait(bar, parity))
-            if ((uint32_t)clock() - t0 > limit) break;
+            if ((uint32_t)clock() - t0 > 4200000000u) break;
     };
     // the CTA's k-th block, looked up by warp 14 for all roles
     const TileWork* works = reinterpret_cast<const TileWork*>(smem + C::kWork);
@@ -465,7 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t id_o = idesc_16<F16>(kTile, D, true);
             // blocks and key tiles that ran on the two row tiles; tile 1 may be left out of a block
             uint32_t unit = 0, nb0 = 0, nb1 = 0, nt0 = 0, nt1 = 0;
-            bool ok = true;
+            bool ok = p.debug_fault != 1;
+            if (!ok) *abort_flag = 2;
             for (int k = 0; ok && next_work(k); ++k) {
                 const int T = w.t1 - w.t0, nq = w.ntok > g.tpt ? 2 : 1;
                 if (T == 0) continue;
@@ -565,9 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-            if (!ok)  // the CTA gives up: its copies in flight land before it ends
-                for (uint32_t u = unit > C::kStages ? unit - C::kStages : 0; u < unit; ++u)
-                    drain(BAR(kv_full, u % C::kStages), (u / C::kStages) & 1);
+            for (uint32_t u = unit > C::kStages ? unit - C::kStages : 0; u < unit; ++u)
+                drain(BAR(kv_full, u % C::kStages), u / C::kStages);
         } else if (warp == 14) {
             // ---------------------------------------------------------------- blocks and queries
             uint32_t nb0 = 0, nb1 = 0;
@@ -606,10 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (q) ++nb1; else ++nb0;
                 }
             }
-            if (!ok) {
-                if (nb0) drain(BAR(q_full, 0), (nb0 - 1) & 1);
-                if (nb1) drain(BAR(q_full, 1), (nb1 - 1) & 1);
-            }
+            if (nb0) drain(BAR(q_full, 0), nb0 - 1);
+            if (nb1) drain(BAR(q_full, 1), nb1 - 1);
         } else {
             // ---------------------------------------------------------------- dead rows of V
             uint32_t unit = 0;

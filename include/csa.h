@@ -495,8 +495,10 @@ int csa_index_topk_noalloc(const csa_dims* dims, const csa_seq* seqs, const csa_
  * attention kernel's first loader warp skip its arrival on the first key tile of every CTA, so that
  * tile never becomes full and the waits on it run out; fault = 2 makes the top-k select of
  * hybrid_attn_decode publish no per-query ready word, so the front attention items' waits on those
- * words run out; fault = 0 turns injection off.
- * wait_limit_ns > 0 sets the limit of the attention kernel's waits (0 restores the default of 2 s).
+ * words run out; fault = 0 turns injection off.  Under fault = 1 the first wait for keys of every CTA of
+ * csa_window_attn and csa_prefix_attn counts as run out, while the copy it waits for is in flight.
+ * wait_limit_ns > 0 sets the limit of the attention kernels' waits (0 restores the default of 2 s; a CTA
+ * that winds down waits for its copies under the default).
  * Process-wide; applies to launches issued after the call.  Returns CSA_OK or
  * CSA_ERR_ARG. */
 int csa_debug_inject(int fault, int64_t wait_limit_ns);

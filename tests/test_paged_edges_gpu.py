@@ -1,9 +1,10 @@
 """Cases of the paged key/value operators at the edges of their contracts: softmax weights far below a row's
-largest one."""
+largest one, waits that run out."""
 import pytest
 import torch
 
 import compressed_sparse_kv_overlapped_b200 as csa
+from tests.paged_harness import SENTINEL, Case, World
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +66,27 @@ def test_weights_far_below_the_first_tokens(dtype, kernel, a, keys):
     assert (e <= tol).all(), f"off by {(e / tol).max():.1f} of the bound, {(e / ref.abs()).mean():.4f} of the value"
     ref_lse = sums.log()[..., 0].repeat(B, 1)
     assert ((lse.double() - ref_lse).abs() <= rel[..., 0].repeat(B, 1) + 2.0 ** -22 * ref_lse).all()
+
+
+@pytest.mark.parametrize("seqs,prefix,direct", [
+    ([(1, 300), (2, 90)], 0, True), ([(1, 9001)], 0, False), ([(90, 300), (64, 64)], 0, True), ([(130, 9001)], 0, False),
+    ([(1, 200), (100, 250)], 0, True), ([(1, 700), (3, 612), (1, 650)], 600, False), ([(90, 900), (1, 700)], 600, False)])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (HF, 64)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(seqs, prefix, direct, dtype, d):
+    """Every CTA's first wait for keys counts as run out while its copies are in flight: the kernels wind down and
+    report it, blocks that write their rows directly leave them alone, and the same call is right afterwards."""
+    w = World(Case(seqs, H=8, H_kv=2, d=d, page=32, dtype=dtype, W=1 << 20, prefix=prefix))
+    args = w.args()
+    ws = w.kv.workspace(args)
+    try:
+        csa.csa_debug_inject(1, 1_000_000)  # 1 ms limit
+        for _ in range(3):
+            w.attend(args, ws)
+        assert csa.csa_sync_status() == csa.CSA_ERR_TIMEOUT
+        if direct:
+            assert (w.out == SENTINEL).all() and (w.lse == SENTINEL).all()
+    finally:
+        csa.csa_debug_inject(0, 0)
+    w.attend(args, ws)
+    assert csa.csa_sync_status() == csa.CSA_OK
+    w.check()
