@@ -10,14 +10,15 @@ H_kv key/value heads): the local and full-attention layers beside a model's comp
 
 The tensors stay the caller's: PagedKV checks them once and fills the C structs.  The ``*_args`` methods
 return the arguments of one call, which can be used again as long as the tensors in them live (they are
-kept alive by the arguments); the tables' contents may change between calls, also between replays of a
-captured graph.  ``append`` writes new tokens (turning keys and queries by position), ``window_attn`` and
+kept alive by the arguments, and go with them: on a stream other than the tensors' own, drop the
+arguments only after the call's work is done); the tables' contents may change between calls, also between
+replays of a captured graph.  ``append`` writes new tokens (turning keys and queries by position), ``window_attn`` and
 ``prefix_attn`` attend them.  Calls run on the current stream of the cache's device unless given one.
 Torch is used for allocation and checks only.
 """
 from __future__ import annotations
 
-import ctypes
+from ctypes import byref
 
 from . import (CSA_KV_BF16, CSA_KV_F16, CSA_OP_PREFIX_ATTN, CSA_OP_WINDOW_ATTN, _check, csa_kv_append_args,
                csa_kv_attn_args, csa_kv_cache, csa_workspace_size, lib)
@@ -92,7 +93,7 @@ class PagedKV:
                   inv_freq.device == self.device, "inv_freq is a contiguous float32 vector on the cache's device")
             a.inv_freq, a.rot = inv_freq.data_ptr(), 2 * inv_freq.numel()
         a.interleaved = 1 if interleaved else 0
-        a._keep, a._ref = (self, k, v, q, q_out, inv_freq), ctypes.byref(a)
+        a._keep = (self, k, v, q, q_out, inv_freq)
         return a
 
     def _attn_args(self, q, out, max_n, max_len, lse, scale):
@@ -109,7 +110,7 @@ class PagedKV:
             _need(lse.dtype == torch.float32 and lse.shape == (q.shape[0], self.H) and lse.is_contiguous() and
                   lse.device == self.device, "lse is a contiguous float32 [rows, H] tensor on the cache's device")
             a.lse = lse.data_ptr()
-        a._keep, a._ref = (self, q, out, lse), ctypes.byref(a)
+        a._keep = (self, q, out, lse)
         return a
 
     def window_args(self, q, out, *, W, S=0, max_n, max_len=None, lse=None, scale=None) -> csa_kv_attn_args:
@@ -156,12 +157,12 @@ class PagedKV:
             _check(rc, name)
 
     def append(self, args: csa_kv_append_args, stream=None) -> None:
-        self._call("csa_kv_append", self._append_fn, stream, args._ref)
+        self._call("csa_kv_append", self._append_fn, stream, byref(args))
 
     def window_attn(self, args: csa_kv_attn_args, ws, stream=None) -> None:
         ptr, size = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
-        self._call("csa_window_attn", self._window_fn, stream, args._ref, ptr, size)
+        self._call("csa_window_attn", self._window_fn, stream, byref(args), ptr, size)
 
     def prefix_attn(self, args: csa_kv_attn_args, ws, stream=None) -> None:
         ptr, size = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
-        self._call("csa_prefix_attn", self._prefix_fn, stream, args._ref, ptr, size)
+        self._call("csa_prefix_attn", self._prefix_fn, stream, byref(args), ptr, size)
