@@ -50,6 +50,9 @@ int check_rows(int64_t rows, int64_t max_n) {
     return CSA_OK;
 }
 
+// No query anywhere by the host's bounds: the call does nothing.
+bool no_rows(const csa_kv_attn_args& a) { return a.rows == 0 || a.max_n == 0 || a.max_len == 0; }
+
 // Shape checks of an attention call; op: CSA_OP_WINDOW_ATTN or CSA_OP_PREFIX_ATTN.
 int check_attn(const csa_kv_attn_args& a, int op) {
     int rc = check_cache(a.kv, false);
@@ -156,6 +159,10 @@ int stream_splits(int64_t items, int64_t keys, bool even, bool merged, int d, in
 
 PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
     PagedPlan pl{};
+    if (no_rows(a)) {
+        pl.total = 256;
+        return pl;
+    }
     const int64_t G = a.kv.H / a.kv.H_kv, cap = a.kv.max_pages * a.kv.page_size, B = a.kv.B;
     const int64_t max_len = a.max_len < cap ? a.max_len : cap;
     const int64_t n = a.max_n < a.rows ? a.max_n : a.rows;  // (what the kernels bound a sequence's n by)
@@ -216,7 +223,7 @@ int run_attn(const csa_kv_attn_args* a, int op, void* ws, size_t ws_bytes, cudaS
     if (!a) return set_error(CSA_ERR_ARG, "args is NULL");
     int rc = check_attn(*a, op);
     if (rc) return rc;
-    if (a->rows == 0 || a->max_n == 0 || a->max_len == 0) return CSA_OK;  // no query anywhere
+    if (no_rows(*a)) return CSA_OK;
     if ((rc = check_cache(a->kv, true))) return rc;
     if (!a->q || !a->out) return set_error(CSA_ERR_ARG, "NULL pointer argument");
     if (!aligned16(a->q) || !aligned16(a->out) || (reinterpret_cast<uintptr_t>(a->lse) & 3u))

@@ -396,7 +396,9 @@ typedef struct csa_kv_attn_args {
     csa_kv_cache kv;
     int64_t rows;        /* rows of the token arrays */
     int64_t max_n;       /* host bound of every sequence's n */
-    int64_t max_len;     /* host bound of every sequence's len (sizes the split of long rows) */
+    int64_t max_len;     /* host bound of every sequence's len: sizes the split of long rows; a sequence beyond it
+                          * is attended all the same.  With max_len = 0, max_n = 0 or rows = 0 no sequence has a
+                          * query: the call does nothing */
     int64_t W;           /* csa_window_attn: window, >= 1 (the token itself counts); else 0 */
     int64_t S;           /* csa_window_attn: first tokens that stay visible, >= 0; else 0 */
     int64_t prefix_len;  /* csa_prefix_attn: tokens of the shared prefix, >= 0; else 0 */

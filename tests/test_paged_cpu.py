@@ -162,3 +162,15 @@ def test_workspace_of_prompts_beside_long_single_rows(lib):
     n = csa.csa_workspace_size(csa.CSA_OP_WINDOW_ATTN, a)
     # at most 64 query rows of each key head of each sequence, at most 256 splits, 516 bytes a row
     assert 256 < n <= 3 * 64 * 8 * 256 * 516 + 4096
+
+
+@pytest.mark.parametrize("kw", [dict(rows=0), dict(max_n=0), dict(rows=0, max_n=0), dict(max_len=0)])
+def test_workspace_of_empty_calls(lib, kw):
+    """A call without rows plans nothing: the least workspace, which the call then takes."""
+    for op, more in ((csa.CSA_OP_WINDOW_ATTN, {}), (csa.CSA_OP_PREFIX_ATTN, dict(W=0, S=0)),
+                     (csa.CSA_OP_PREFIX_ATTN, dict(W=0, S=0, prefix_len=40))):
+        a = attn_args(**{**more, **kw})
+        n = csa.csa_workspace_size(op, a)
+        assert n == 256
+        call = lib.csa_window_attn if op == csa.CSA_OP_WINDOW_ATTN else lib.csa_prefix_attn
+        assert call(ctypes.byref(a), 256, n, None) == csa.CSA_OK
