@@ -156,13 +156,19 @@ class PagedKV:
         if rc:
             _check(rc, name)
 
+    def _space(self, ws):
+        if ws is None:
+            return None, 0
+        if ws.get_device() != self._device_index or not ws.is_contiguous():
+            raise ValueError(f"the workspace is a contiguous tensor on {self.device}, got one on {ws.device} with strides "
+                             f"{ws.stride()}")
+        return ws.data_ptr(), ws.nbytes
+
     def append(self, args: csa_kv_append_args, stream=None) -> None:
         self._call("csa_kv_append", self._append_fn, stream, byref(args))
 
     def window_attn(self, args: csa_kv_attn_args, ws, stream=None) -> None:
-        ptr, size = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
-        self._call("csa_window_attn", self._window_fn, stream, byref(args), ptr, size)
+        self._call("csa_window_attn", self._window_fn, stream, byref(args), *self._space(ws))
 
     def prefix_attn(self, args: csa_kv_attn_args, ws, stream=None) -> None:
-        ptr, size = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
-        self._call("csa_prefix_attn", self._prefix_fn, stream, byref(args), ptr, size)
+        self._call("csa_prefix_attn", self._prefix_fn, stream, byref(args), *self._space(ws))

@@ -49,3 +49,31 @@ def test_dropped_arguments_free_their_tensors_at_once(call):
     finally:
         if enabled:
             gc.enable()
+
+
+class Refused(Exception):
+    pass
+
+
+def no_call(*a):
+    raise Refused("the library was called")
+
+
+@pytest.mark.parametrize("call", ["window_attn", "prefix_attn"])
+def test_a_workspace_elsewhere_is_refused(call):
+    """A workspace that the kernels cannot reach, or that is not one run of bytes, never gets to a launch."""
+    kv = handle()
+    q, out = tokens(H), tokens(H)
+    args = kv.window_args(q, out, W=8, max_n=3) if call == "window_attn" else kv.prefix_args(q, out, prefix_len=8, max_n=3)
+    kv._device_index, kv._window_fn, kv._prefix_fn = 0, no_call, no_call
+    kv._current_stream, kv._current_device = (lambda i: 0), (lambda: 0)
+    kv.device = torch.device("cuda", 0)
+    run = getattr(kv, call)
+    with pytest.raises(ValueError, match="workspace"):
+        run(args, torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="workspace"):
+        run(args, torch.empty(1, dtype=torch.uint8).expand(1 << 20))
+    with pytest.raises(ValueError, match="workspace"):
+        run(args, torch.empty(1 << 20, dtype=torch.uint8, device="meta"))
+    with pytest.raises(Refused):  # (none at all is the library's to judge)
+        run(args, None)
