@@ -341,7 +341,7 @@ int hybrid_attn_prefill(const csa_prefill_args* args, void* ws, size_t ws_bytes,
 /* One sequence of a call, device memory: its new tokens are the rows [row, row + n) of the call's token
  * arrays (q, k, v, out, lse), the newest n of the `len` tokens it holds (new ones included): row
  * row + i is position len - n + i.  n = 0 leaves the sequence out.  Rows that belong to no sequence are
- * neither read nor written.  An entry with n < 0, n > max_n, len < n, len > max_pages * page_size or
+ * not written; their queries may be read, hold any bits and change no result.  An entry with n < 0, n > max_n, len < n, len > max_pages * page_size or
  * rows outside [0, rows) is reported as CSA_ERR_INDEX and the sequence is skipped. */
 typedef struct csa_kv_seq {
     int64_t row;
@@ -428,7 +428,8 @@ int csa_window_attn(const csa_kv_attn_args* args, void* ws, size_t ws_bytes, csa
  * by log-sum-exp.  prefix_len need not end on a page: the tokens behind it in that page are each
  * sequence's own, in its own copy of the page.  Every sequence with n > 0 needs len - n >= prefix_len
  * (else CSA_ERR_INDEX on the device and the sequence is skipped).  Row 0 of the table must hold the
- * prefix even if its sequence is left out.  Workspace: CSA_OP_PREFIX_ATTN. */
+ * prefix even if its sequence is left out.  The prefix is attended for all `rows` rows, those of no
+ * sequence too, so a call padded to more rows pays for them.  Workspace: CSA_OP_PREFIX_ATTN. */
 int csa_prefix_attn(const csa_kv_attn_args* args, void* ws, size_t ws_bytes, csa_stream_t stream);
 
 /* Workspace sizes.  `op` selects the call and `args` points to the arguments it describes:

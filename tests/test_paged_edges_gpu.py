@@ -1,5 +1,5 @@
 """Cases of the paged key/value operators at the edges of their contracts: softmax weights far below a row's
-largest one, waits that run out."""
+largest one, waits that run out, queries of rows that no sequence has."""
 import pytest
 import torch
 
@@ -88,5 +88,20 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(seqs, prefi
     finally:
         csa.csa_debug_inject(0, 0)
     w.attend(args, ws)
+    assert csa.csa_sync_status() == csa.CSA_OK
+    w.check()
+
+
+@pytest.mark.parametrize("seqs,prefix", [([(1, 300), (2, 90), (0, 40)], 0), ([(90, 300), (64, 64)], 0), ([(1, 700), (3, 612), (0, 650)], 600),
+                                         ([(90, 900), (1, 700)], 600)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_queries_of_no_sequence_change_nothing(seqs, prefix, value):
+    """Rows between the sequences, and those of a sequence that is left out, hold no numbers."""
+    w = World(Case(seqs, H=8, H_kv=2, d=64, page=32, W=1 << 20, prefix=prefix, gap=3))
+    mine = torch.zeros(w.rows, dtype=torch.bool)
+    for row, n, _ in w.seq_rows:
+        mine[row:row + n] = True
+    w.q[~mine.to(w.q.device)] = value
+    w.attend()
     assert csa.csa_sync_status() == csa.CSA_OK
     w.check()
