@@ -462,23 +462,26 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
         const float mine = base + ln < slots ? fast_exp2(sum_at(base + ln) - mu) : 0.f;
         const int cnt = slots - base < kLanes ? slots - base : kLanes;
         for (int j0 = 0; j0 < cnt; j0 += 8) {  // eight loads in flight
+            float w[8];
             float4 x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int slot = base + j0 + j < slots ? base + j0 + j : slots - 1;
-                x[j] = *reinterpret_cast<const float4*>(
-                    (slot < first ? m.prefix.o + (at + slot * m.prefix.rows * kv.H) * D
-                                  : own.o + (at_own + (slot - first) * own.rows * kv.H) * D) + c);
+                const int slot = base + j0 + j;
+                w[j] = __shfl_sync(mask, mine, j0 + j, kLanes);
+                // (0 past the last, or of an empty partial, whose output was not written: not read either)
+                x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (w[j] != 0.f)
+                    x[j] = *reinterpret_cast<const float4*>(
+                        (slot < first ? m.prefix.o + (at + slot * m.prefix.rows * kv.H) * D
+                                      : own.o + (at_own + (slot - first) * own.rows * kv.H) * D) + c);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float w = __shfl_sync(mask, mine, j0 + j, kLanes);
-                if (w == 0.f) continue;  // (past the last, or an empty partial, whose output was not written)
-                sum += w;
-                acc.x = fmaf(x[j].x, w, acc.x);
-                acc.y = fmaf(x[j].y, w, acc.y);
-                acc.z = fmaf(x[j].z, w, acc.z);
-                acc.w = fmaf(x[j].w, w, acc.w);
+                sum += w[j];
+                acc.x = fmaf(x[j].x, w[j], acc.x);
+                acc.y = fmaf(x[j].y, w[j], acc.y);
+                acc.z = fmaf(x[j].z, w[j], acc.z);
+                acc.w = fmaf(x[j].w, w[j], acc.w);
             }
         }
     }

@@ -105,3 +105,22 @@ def test_queries_of_no_sequence_change_nothing(seqs, prefix, value):
     w.attend()
     assert csa.csa_sync_status() == csa.CSA_OK
     w.check()
+
+
+@pytest.mark.parametrize("prefix", [0, 600])
+def test_empty_partials_are_not_used(prefix):
+    """Sequences far below the bound on lengths leave most splits empty: the workspace holds NaN there, which is neither
+    read nor weighed."""
+    w = World(Case([(1, 700), (2, 950), (1, 601), (1, 640)], H=8, H_kv=1, d=128, page=64, W=1 << 20, prefix=prefix))
+    args = w.kv.prefix_args(w.q, w.out, prefix_len=prefix, max_n=2, lse=w.lse, scale=w.scale) if prefix else \
+        w.kv.window_args(w.q, w.out, W=1 << 20, max_n=2, lse=w.lse, scale=w.scale)
+    args.max_len = 60000
+    args.kv.max_pages = 1024
+    w.table = torch.nn.functional.pad(w.table, (0, 1024 - w.table.shape[1]), value=-1)
+    args.kv.page_table = w.table.data_ptr()
+    ws = w.kv.workspace(args)
+    assert ws.numel() > 4 * 8 * 129 * 4 * 8, "at least eight splits"
+    ws.fill_(255)  # NaN in fp32
+    w.attend(args, ws)
+    assert csa.csa_sync_status() == csa.CSA_OK
+    w.check()
