@@ -118,40 +118,54 @@ int tile_splits(int64_t items, int64_t keys, int sms) {
     return tiles > 0 ? (int)((tiles + each - 1) / each) : 1;
 }
 
+// What the host knows of the keys that the sequences of a launch see: all the same (a shared prefix), bounded by a
+// window that most of them fill, or only that none has more than the bound.
+enum class Lengths { same, window, bound };
+
 // The stream kernel's cut: splits of `groups` 16-key groups each, for `items` blocks that see up to `keys`
 // keys.  Lengths are known on the device only, so a split is a fixed number of keys: a shorter sequence
 // has fewer.  The number is the one with the least estimated time, in us: blocks run in rounds of two an
 // SM; a round takes its bytes at 6.4 TB/s, but no less than a block alone needs, 60 keys a us, and 1.5 to
-// start; a merge that would not be there otherwise costs 6, each split of a row 1 (0.25 beside a prefix).
-// Rows of 4,096 keys, 80 / 128 / 256 / 320 / 384 / 512 blocks: 48 / 71 / 108 / 142 / 157 / 191 us; cut for two
-// rounds whenever one is not full 60 / 83 / 120 / 181 / 184 / 191, uncut 78 / 78 / 106 / 182 / 184 / 188.
-// Where lengths may differ much (`even` is false: the window does not bound them) a split has 2,048 keys at
-// most, else 8,192, lest long sequences outlast the rest: causal rows of 1,000 to 8,000 keys, 512 blocks:
-// 212 us, uncut 246.  Long rows, where partials cost little, have two rounds of blocks whatever the estimate
-// says: five sequences of 40,000 to 131,072, window 65,536: 15 splits 214 us, 7 splits 234, 17 splits 246, 30
-// splits 225.  Never more than `most` splits.
-int stream_splits(int64_t items, int64_t keys, bool even, bool merged, int d, int sms, int64_t most, int* groups) {
-    constexpr int64_t kRagged = 2048, kEven = 8192;
-    constexpr double kBytesUs = 6.4e6, kKeysUs = 60.0, kStartUs = 1.5;
+// start; a merge that would not be there otherwise costs 6, each split of a row 0.5 (0.25 beside a prefix).
+// A tenth of the estimate under a window is that of a batch with half of the keys, whose time ends with one long
+// row's last block.
+// A split has at most 2,048 keys (8,192 where lengths are the same or bounded by a window), lest one long sequence
+// outlast the rest, or a 32nd of the bound, lest a loose bound ask for blocks and partials of nothing.
+// Beyond what that asks for there are never more than `most` splits.
+// Measured with 8 key heads of 128, in us.
+//   Windows of 4,096, 80 / 128 / 256 / 320 / 384 / 512 blocks: 47 / 68 / 107 / 141 / 154 / 188; uncut 78 / 78 / 107 /
+//     182 / 184 / 188.
+//   Five windows of 65,536: 14 splits 230 (6: 222, 7: 232, 15: 271); one of them of 40,000: 220 (7: 212, 15: 214).
+//   Windows of 16,384, 31 sequences of 1,000 and one of 131,072: 8 splits 73 (2: 161, uncut 283).
+//   Windows of 12,000, 32 full ones, where the cap costs: 2 splits 265 (uncut 244).
+//   Causal, 31 sequences of 1,000 and one of 131,072: 32 splits 160 (64: 194, 8: 323, 3: 599).
+//   Causal, 32 sequences of 1,000 to 32,768: 15 splits 339 (7: 353, 3: 392).
+//   Causal, 128 sequences of 8,000: 4 splits 645; with a bound of 2^20: 32 splits 729 (256: 1,592).
+int stream_splits(int64_t items, int64_t keys, Lengths lengths, bool merged, int d, int sms, int64_t most, int* groups) {
+    constexpr int64_t kLongest = 2048, kLongestEven = 8192, kAsked = 32;
+    constexpr double kBytesUs = 6.4e6, kKeysUs = 60.0, kStartUs = 1.5, kShortShare = 0.1;
     const int64_t places = 2 * (int64_t)sms;
     const int64_t least = items * (keys / 128) <= places ? 128 : 256;  // keys of a split
-    const int64_t longest = even ? kEven : kRagged, from = keys > longest ? (keys + longest - 1) / longest : 1;
+    const int64_t longest = lengths == Lengths::bound ? kLongest : kLongestEven;
+    int64_t from = keys > longest ? (keys + longest - 1) / longest : 1;
+    if (from > kAsked) from = kAsked;
+    const int64_t fill = (places + items - 1) / items, upto = fill > 64 ? fill : 64;
     int64_t s = from;
     double best = 1e30;
-    for (int64_t i = from; i == from || (i <= 64 && i * least <= keys); ++i) {
+    for (int64_t i = from; i == from || (i <= upto && i * least <= keys); ++i) {
         const double share = (double)keys / (double)i, alone = share / kKeysUs, us = share * 4.0 * d / kBytesUs;
         const int64_t full = items * i / places, rest = items * i % places;
         double t = (double)full * (((double)places * us > alone ? (double)places * us : alone) + kStartUs);
         if (rest) t += ((double)rest * us > alone ? (double)rest * us : alone) + kStartUs;
-        if (i > 1) t = 1.05 * t + (merged ? 0.25 * (double)i : 6.0 + (double)i);  // (a cut has to be worth it)
+        if (lengths == Lengths::window)
+            t += kShortShare * (0.5 * (double)(items * i) * us + alone + kStartUs - t);
+        if (i > 1) t = 1.05 * t + (merged ? 0.25 * (double)i : 6.0 + 0.5 * (double)i);  // (a cut has to be worth it)
         if (t < best) {
             best = t;
             s = i;
         }
     }
-    const int64_t two = items > 0 ? (2 * places + items - 1) / items : 1;  // splits for two rounds
-    if (items < places && keys >= two * kRagged) s = two;
-    if (s > most) s = most;
+    if (s > most) s = most > from ? most : from;
     const int64_t n = keys / 16 + 2;  // (both runs of keys may begin and end inside a group)
     *groups = (int)((n + s - 1) / s);
     return (int)((n + *groups - 1) / *groups);
@@ -178,10 +192,11 @@ PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
     };
     const bool prefix = op == CSA_OP_PREFIX_ATTN && a.prefix_len > 0;
     if (pl.few) {
-        // (beside prompts most sequences may have none of these rows: no more than one round of blocks)
+        // (beside prompts most sequences may have none of these rows: no more than one round of blocks, but for the
+        // cap on a split's keys)
         const int64_t items = stream_items(B, n_few), one_round = 2 * (int64_t)sms / items;
-        pl.splits_few = stream_splits(items, keys(n_few), op == CSA_OP_WINDOW_ATTN && a.W < max_len, prefix, a.kv.d, sms,
-                                      pl.many ? (one_round > 1 ? one_round : 1) : 256, &pl.few_groups);
+        const Lengths lengths = op == CSA_OP_WINDOW_ATTN && a.W < max_len ? Lengths::window : Lengths::bound;
+        pl.splits_few = stream_splits(items, keys(n_few), lengths, prefix, a.kv.d, sms, pl.many ? one_round : 256, &pl.few_groups);
     }
     if (pl.many) {
         int64_t blocks = B * ((n + tpb - 1) / tpb);
@@ -192,7 +207,7 @@ PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
         pl.prefix_tile = a.rows * G > kFewPrefixRows;
         pl.splits_prefix = pl.prefix_tile
                                ? tile_splits(a.kv.H_kv * ((a.rows + tpb - 1) / tpb), a.prefix_len, sms)
-                               : stream_splits(stream_items(1, a.rows), a.prefix_len, true, true, a.kv.d, sms, 256,
+                               : stream_splits(stream_items(1, a.rows), a.prefix_len, Lengths::same, true, a.kv.d, sms, 256,
                                                &pl.prefix_groups);
     }
     // partials of the prefix for all rows; of a class of sequences where it is split or has a prefix, those of

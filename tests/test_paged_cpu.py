@@ -174,3 +174,39 @@ def test_workspace_of_empty_calls(lib, kw):
         assert n == 256
         call = lib.csa_window_attn if op == csa.CSA_OP_WINDOW_ATTN else lib.csa_prefix_attn
         assert call(ctypes.byref(a), 256, n, None) == csa.CSA_OK
+
+
+def splits_of(a, op=csa.CSA_OP_WINDOW_ATTN):
+    """Key splits of the rows of a batch of single tokens, from the workspace: d + 1 floats a row, head and split."""
+    per = a.kv.B * a.kv.H * (a.kv.d + 1) * 4
+    n = csa.csa_workspace_size(op, a)
+    return 1 if n <= per else round(n / per)
+
+
+def decode(B, max_len, W=1 << 40, H_kv=8, d=128):
+    kv = cache(H=8 * H_kv, H_kv=H_kv, d=d, B=B, page_size=64, max_pages=1 << 15, num_pages=1 << 20, page_stride=64 * H_kv * d,
+               slot_stride=H_kv * d, head_stride=d)
+    return attn_args(kv, rows=B, max_n=1, max_len=max_len, W=W, S=0, q_stride=8 * H_kv * d, out_stride=8 * H_kv * d)
+
+
+@pytest.mark.parametrize("B", [1, 3, 5, 8, 16, 31, 32, 33, 64, 128, 300])
+@pytest.mark.parametrize("H_kv,d", [(8, 128), (2, 128), (8, 64), (1, 64)])
+def test_no_split_outlasts_the_batch(lib, B, H_kv, d):
+    """Keys of a split: at most 2,048, or 8,192 under a window, or a 32nd of the bound on the keys, whatever the number
+    of sequences; and never so many splits that a loose bound fills the workspace."""
+    for keys in (100, 1000, 2048, 2049, 6000, 6200, 8192, 10000, 16384, 40000, 65536, 70000, 131072, 1 << 20):
+        for window in (False, True):
+            s = splits_of(decode(B, 1 << 21 if window else keys, keys if window else 1 << 40, H_kv, d))
+            longest = max(8192 if window else 2048, -(-keys // 32))
+            assert s * (longest + 32) >= keys, (keys, window, s)
+            # (what fills two blocks on each of 148 SMs may be more)
+            assert s <= max(64, -(-296 // (B * H_kv))) and s <= 256, (keys, window, s)
+
+
+def test_few_long_rows_beside_prompts_are_split(lib):
+    """The same cap where prompts are in the call: a continuous batch of 64 sequences, one of them long."""
+    a = decode(64, 131072)
+    a.rows, a.max_n = 64 + 512, 512
+    # 8 tokens of each sequence belong to the kernel of few rows
+    per = 64 * 8 * 64 * 129 * 4
+    assert csa.csa_workspace_size(csa.CSA_OP_WINDOW_ATTN, a) >= 32 * per

@@ -124,3 +124,16 @@ def test_empty_partials_are_not_used(prefix):
     w.attend(args, ws)
     assert csa.csa_sync_status() == csa.CSA_OK
     w.check()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (HF, 64)])
+def test_one_long_row_in_a_wide_batch_beside_a_prompt(dtype, d):
+    """The long row's keys are cut, the prompt's rows are written directly."""
+    c = Case([(1, 50 + i) for i in range(98)] + [(1, 9000), (300, 400)], H=8, H_kv=1, d=d, page=64, dtype=dtype, W=1 << 20)
+    w = World(c)
+    args = w.args()
+    ws = w.kv.workspace(args)
+    assert ws.numel() >= 4 * 100 * 8 * 8 * (d + 1) * 4, "four splits of eight rows of each sequence"
+    w.attend(args, ws)
+    assert csa.csa_sync_status() == csa.CSA_OK
+    w.check()
