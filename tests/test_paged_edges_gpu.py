@@ -137,3 +137,31 @@ def test_one_long_row_in_a_wide_batch_beside_a_prompt(dtype, d):
     w.attend(args, ws)
     assert csa.csa_sync_status() == csa.CSA_OK
     w.check()
+
+
+@pytest.mark.parametrize("prefix", [0, 100])
+def test_module_functions_make_the_same_calls(prefix):
+    """csa_kv_append, csa_window_attn and csa_prefix_attn of the module, beside the methods of PagedKV."""
+    c = Case([(2, 3000), (70, 300)], H=8, H_kv=2, d=64, page=32, W=1 << 20, prefix=prefix)
+    results = []
+    for methods in (True, False):
+        w = World(c, all_live=True)
+        g = torch.Generator().manual_seed(2)
+        k, v = (torch.randn(w.rows, c.H_kv, c.d, generator=g).to(c.dtype).cuda() for _ in range(2))
+        turned = torch.empty_like(w.q)
+        inv = (10000.0 ** (-torch.arange(0, c.d, 2) / c.d)).float().cuda()
+        a = w.kv.append_args(k, v, w.q, turned, max_n=w.max_n, inv_freq=inv)
+        kw = dict(max_n=w.max_n, max_len=w.max_len, lse=w.lse, scale=w.scale)
+        b = w.kv.prefix_args(turned, w.out, prefix_len=prefix, **kw) if prefix else w.kv.window_args(turned, w.out, W=c.W, **kw)
+        ws = w.kv.workspace(b)
+        if methods:
+            w.kv.append(a)
+            w.attend(b, ws)
+        else:
+            csa.csa_kv_append(a)
+            (csa.csa_prefix_attn if prefix else csa.csa_window_attn)(b, ws)
+        assert csa.csa_sync_status() == csa.CSA_OK
+        results.append([w.kp, w.vp, turned, w.out, w.lse])
+    for x, y in zip(*results):
+        assert torch.equal(x.nan_to_num(9.0), y.nan_to_num(9.0))
+    assert not results[0][3].isnan().any()
