@@ -90,7 +90,7 @@ struct PagedPlan {
 
 // Rows of one key head up to which the stream kernel is used.  It reads a block's keys once per 32 rows,
 // the tile kernel once per 256 but with at least a tile's time (2 us) per 128 keys: 128 rows on a prefix of
-// 8,192 take 39 us here through the tile kernel and 92 through the stream kernel; up to 64 rows, where
+// 8,192 take 37 us here through the tile kernel and 92 through the stream kernel; up to 64 rows, where
 // long rows are split over all SMs, the stream kernel's launch is the shorter one.
 constexpr int64_t kFewRows = 64;
 constexpr int64_t kFewPrefixRows = 64;  // the same for the rows of all sequences on the prefix

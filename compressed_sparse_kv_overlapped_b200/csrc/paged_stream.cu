@@ -21,11 +21,11 @@
 // two products run on mma.sync m16n8k16: the tensor pipe is far from a limit here (32 of them per
 // 8 KiB at d = 128, 19 % busy) and tcgen05 would want 128 rows.
 //
-// Measured (d = 128, 8 key heads): five sequences with a window of 65,536, 1.24 GB in 193 us = 6.4 TB/s
-// (0.98 of the copy rate) and 214 us with the merge; 32 sequences with a window of 4,096, 538 MB in 94 us
-// = 5.7 TB/s; one short row 5.8 us, a chain of latencies (tables, copy, merge of the
-// warps).  Copies by cp.async from eight warps of one block an SM took 324, 115 and 6.1 us: some 700
-// instructions a group, most of them addresses.
+// Measured (d = 128, 8 key heads): five sequences with a window of 65,536, 1.24 GB in 206 us = 6.0 TB/s
+// (0.92 of the copy rate) and 221 us with the merge; 32 sequences with a window of 4,096, 538 MB in 92 us
+// = 5.8 TB/s; one short row 8.2 us a call, a chain of latencies (tables, copy, merge of the warps).
+// Copies by cp.async from eight warps of one block an SM took 324, 115 and 6.2 us: some 700 instructions a
+// group, most of them addresses, but a shorter start.
 #include "paged.h"
 #include "tma.h"
 

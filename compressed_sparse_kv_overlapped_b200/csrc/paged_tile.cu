@@ -20,15 +20,16 @@
 // loaded whole; their dead rows of V are zeroed in shared memory before the product (a weight of zero
 // does not remove a NaN), their dead scores by selection.
 //
-// CTAs are persistent, one per SM, and all rings run on across blocks: the next block's Q, keys and
-// first scores overlap this one's last product and its epilogue.  Blocks are taken longest first, in
-// alternating order, so that the CTAs' sums stay close for causal prompts.
+// CTAs are persistent, one per SM, and all rings run on across blocks: the next block's Q and keys arrive
+// during this one's last products, behind which its first scores are issued (those of both row tiles, so
+// that the tiles start a block together), and both overlap this one's epilogue.  Blocks are taken longest
+// first, in alternating order, so that the CTAs' sums stay close for causal prompts.
 //
 // Warps: 0-3 / 4-7 softmax of tile 0 / 1, 8-11 epilogue, 12 MMA issuer, 13 key loader, 14 look-up of
 // the blocks and query loader, 15 zeroing of dead V rows.  Every wait is bounded and winds the CTA down.
 //
-// Measured (bf16, d = 128): causal prompts of 77 to 8,191 tokens, 32 heads on 8, 0.84 ms = 0.97 PFLOP/s
-// (0.59 of a cuBLAS GEMM); the tensor pipe is 53 % busy and issue slots 41 %.  Bound by the chain of one
+// Measured (bf16, d = 128): causal prompts of 77 to 8,191 tokens, 32 heads on 8, 0.85 ms = 0.96 PFLOP/s
+// (0.58 of a cuBLAS GEMM); the tensor pipe is 53 % busy and issue slots 41 %.  Bound by the chain of one
 // tile: of its period of about 3,700 clocks the softmax of a row tile takes about 2,500 (512 clocks of
 // loads and maximum, the rest exponentials at 16 a clock and SM, shared with the other tile's) and the
 // products 1,000.  A prompt of 32,768 with a window of 128: 0.44 ms for 1.2 GB (0.42 of the copy rate),
