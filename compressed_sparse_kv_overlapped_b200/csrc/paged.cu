@@ -130,8 +130,8 @@ enum class Lengths { same, window, bound };
 // A tenth of the estimate under a window is that of a batch with half of the keys, whose time ends with one long
 // row's last block.
 // A split has at most 2,048 keys (8,192 where lengths are the same or bounded by a window), lest one long sequence
-// outlast the rest, or a 32nd of the bound, lest a loose bound ask for blocks and partials of nothing.
-// Beyond what that asks for there are never more than `most` splits.
+// outlast the rest.  That asks for no more than `asked` splits, nor than 2^14 blocks, of 4 ns each where they are
+// empty, lest a loose bound fill the grid and the workspace with nothing.  Beyond it there are never more than `most`.
 // Measured with 8 key heads of 128, in us.
 //   Windows of 4,096, 80 / 128 / 256 / 320 / 384 / 512 blocks: 47 / 68 / 107 / 141 / 154 / 188; uncut 78 / 78 / 107 /
 //     182 / 184 / 188.
@@ -140,15 +140,21 @@ enum class Lengths { same, window, bound };
 //   Windows of 12,000, 32 full ones, where the cap costs: 2 splits 265 (uncut 244).
 //   Causal, 31 sequences of 1,000 and one of 131,072: 32 splits 160 (64: 194, 8: 323, 3: 599).
 //   Causal, 32 sequences of 1,000 to 32,768: 15 splits 339 (7: 353, 3: 392).
-//   Causal, 128 sequences of 8,000: 4 splits 645; with a bound of 2^20: 32 splits 729 (256: 1,592).
-int stream_splits(int64_t items, int64_t keys, Lengths lengths, bool merged, int d, int sms, int64_t most, int* groups) {
-    constexpr int64_t kLongest = 2048, kLongestEven = 8192, kAsked = 32;
+//   Causal, 128 sequences of 8,000: 4 splits 645; with a bound of 2^20: 16 splits 695 (32: 729, 256: 1,592).
+//   Beside a prompt of 512, 64 sequences of 1,000, bound 131,072: 16 splits 158 (32: 206, uncut 95); one of them of
+//     131,072: 249 (32: 302, uncut 3,110).
+constexpr int64_t kAsked = 32;
+int stream_splits(int64_t items, int64_t keys, Lengths lengths, bool merged, int d, int sms, int64_t asked, int64_t most,
+                  int* groups) {
+    constexpr int64_t kLongest = 2048, kLongestEven = 8192;
     constexpr double kBytesUs = 6.4e6, kKeysUs = 60.0, kStartUs = 1.5, kShortShare = 0.1;
     const int64_t places = 2 * (int64_t)sms;
     const int64_t least = items * (keys / 128) <= places ? 128 : 256;  // keys of a split
     const int64_t longest = lengths == Lengths::bound ? kLongest : kLongestEven;
     int64_t from = keys > longest ? (keys + longest - 1) / longest : 1;
-    if (from > kAsked) from = kAsked;
+    const int64_t blocks = items < 16384 ? 16384 / items : 1;
+    if (from > asked) from = asked;
+    if (from > blocks) from = blocks;
     const int64_t fill = (places + items - 1) / items, upto = fill > 64 ? fill : 64;
     int64_t s = from;
     double best = 1e30;
@@ -181,6 +187,8 @@ PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
     const int64_t max_len = a.max_len < cap ? a.max_len : cap;
     const int64_t n = a.max_n < a.rows ? a.max_n : a.rows;  // (what the kernels bound a sequence's n by)
     const int64_t n_few = n * G > kFewRows ? kFewRows / G : n, tpb = 2 * (128 / G);
+    const bool by_seq = B * n_few <= a.rows;  // how partials of few rows are held: whichever is less
+    const int64_t few_rows = by_seq ? B * n_few : a.rows;
     const int sms = sm_count_or(148);
     auto stream_items = [&](int64_t seqs, int64_t rows) { return seqs * a.kv.H_kv * ((rows * G + 31) / 32); };
     pl.many = n * G > kFewRows;
@@ -192,11 +200,13 @@ PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
     };
     const bool prefix = op == CSA_OP_PREFIX_ATTN && a.prefix_len > 0;
     if (pl.few) {
-        // (beside prompts most sequences may have none of these rows: no more than one round of blocks, but for the
-        // cap on a split's keys)
+        // (beside prompts most sequences may have none of these rows: no more than one round of blocks but for the cap
+        // on a split's keys, which asks for a gigabyte of partials at most)
         const int64_t items = stream_items(B, n_few), one_round = 2 * (int64_t)sms / items;
+        const int64_t fit = ((int64_t)1 << 30) / (few_rows * a.kv.H * (a.kv.d + 1) * 4), room = fit > 1 ? fit : 1;
         const Lengths lengths = op == CSA_OP_WINDOW_ATTN && a.W < max_len ? Lengths::window : Lengths::bound;
-        pl.splits_few = stream_splits(items, keys(n_few), lengths, prefix, a.kv.d, sms, pl.many ? one_round : 256, &pl.few_groups);
+        pl.splits_few = stream_splits(items, keys(n_few), lengths, prefix, a.kv.d, sms, pl.many && room < kAsked ? room : kAsked,
+                                      pl.many ? one_round : 256, &pl.few_groups);
     }
     if (pl.many) {
         int64_t blocks = B * ((n + tpb - 1) / tpb);
@@ -207,11 +217,11 @@ PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
         pl.prefix_tile = a.rows * G > kFewPrefixRows;
         pl.splits_prefix = pl.prefix_tile
                                ? tile_splits(a.kv.H_kv * ((a.rows + tpb - 1) / tpb), a.prefix_len, sms)
-                               : stream_splits(stream_items(1, a.rows), a.prefix_len, Lengths::same, true, a.kv.d, sms, 256,
-                                               &pl.prefix_groups);
+                               : stream_splits(stream_items(1, a.rows), a.prefix_len, Lengths::same, true, a.kv.d, sms, kAsked,
+                                               256, &pl.prefix_groups);
     }
     // partials of the prefix for all rows; of a class of sequences where it is split or has a prefix, those of
-    // few rows by sequence (the rows of a prompt beside them need none)
+    // few rows by sequence (the rows of a prompt beside them need none) unless the call has fewer rows than that
     auto partials = [&](int splits, int64_t rows, int64_t per_seq) {
         PagedPartials q{};
         q.rows = rows;
@@ -220,7 +230,7 @@ PagedPlan make_plan(const csa_kv_attn_args& a, int op) {
         return q;
     };
     if (pl.splits_prefix) pl.merge.prefix = partials(pl.splits_prefix, a.rows, 0);
-    if (pl.few && (pl.splits_prefix || pl.splits_few > 1)) pl.merge.few = partials(pl.splits_few, B * n_few, n_few);
+    if (pl.few && (pl.splits_prefix || pl.splits_few > 1)) pl.merge.few = partials(pl.splits_few, few_rows, by_seq ? n_few : 0);
     if (pl.many && (pl.splits_prefix || pl.splits_many > 1)) pl.merge.many = partials(pl.splits_many, a.rows, 0);
     for (PagedPartials* q : {&pl.merge.prefix, &pl.merge.few, &pl.merge.many}) {
         const size_t heads = (size_t)q->rows * a.kv.H * q->slots;

@@ -192,12 +192,13 @@ def decode(B, max_len, W=1 << 40, H_kv=8, d=128):
 @pytest.mark.parametrize("B", [1, 3, 5, 8, 16, 31, 32, 33, 64, 128, 300])
 @pytest.mark.parametrize("H_kv,d", [(8, 128), (2, 128), (8, 64), (1, 64)])
 def test_no_split_outlasts_the_batch(lib, B, H_kv, d):
-    """Keys of a split: at most 2,048, or 8,192 under a window, or a 32nd of the bound on the keys, whatever the number
-    of sequences; and never so many splits that a loose bound fills the workspace."""
+    """Keys of a split: at most 2,048, or 8,192 under a window, or a 32nd of the bound on the keys (less often cut where
+    there are more than 512 blocks already); and never so many splits that a loose bound fills the workspace."""
+    asked = min(32, 16384 // (B * H_kv))
     for keys in (100, 1000, 2048, 2049, 6000, 6200, 8192, 10000, 16384, 40000, 65536, 70000, 131072, 1 << 20):
         for window in (False, True):
             s = splits_of(decode(B, 1 << 21 if window else keys, keys if window else 1 << 40, H_kv, d))
-            longest = max(8192 if window else 2048, -(-keys // 32))
+            longest = max(8192 if window else 2048, -(-keys // asked))
             assert s * (longest + 32) >= keys, (keys, window, s)
             # (what fills two blocks on each of 148 SMs may be more)
             assert s <= max(64, -(-296 // (B * H_kv))) and s <= 256, (keys, window, s)
@@ -207,6 +208,27 @@ def test_few_long_rows_beside_prompts_are_split(lib):
     """The same cap where prompts are in the call: a continuous batch of 64 sequences, one of them long."""
     a = decode(64, 131072)
     a.rows, a.max_n = 64 + 512, 512
-    # 8 tokens of each sequence belong to the kernel of few rows
+    # 8 tokens of each sequence belong to the kernel of few rows, 1,024 blocks before the cut
     per = 64 * 8 * 64 * 129 * 4
-    assert csa.csa_workspace_size(csa.CSA_OP_WINDOW_ATTN, a) >= 32 * per
+    assert csa.csa_workspace_size(csa.CSA_OP_WINDOW_ATTN, a) >= 16 * per
+
+
+@pytest.mark.parametrize("B", [2, 16, 64, 256, 1024])
+@pytest.mark.parametrize("H,H_kv", [(64, 8), (64, 64), (32, 1)])
+@pytest.mark.parametrize("chunk", [100, 512, 8192])
+def test_partials_beside_prompts_stay_small(lib, B, H, H_kv, chunk):
+    """A continuous batch of B sequences and a chunk of a prompt: partials are held for the rows of the call or for the
+    short rows of each sequence, whichever is less, and for few splits where even that is much."""
+    d = 128
+    kv = cache(H=H, H_kv=H_kv, d=d, B=B, page_size=64, max_pages=1 << 15, num_pages=1 << 20, page_stride=64 * H_kv * d,
+               slot_stride=H_kv * d, head_stride=d)
+    rows = B - 1 + chunk
+    one = min(rows, B * (64 // (H // H_kv))) * H * (d + 1) * 4  # bytes of a split of the short rows
+    for max_len in (5000, 131072, 1 << 20):
+        a = attn_args(kv, rows=rows, max_n=chunk, max_len=max_len, W=1 << 40, S=0, q_stride=H * d, out_stride=H * d)
+        n = csa.csa_workspace_size(csa.CSA_OP_WINDOW_ATTN, a)
+        # the chunk itself is cut while its blocks are fewer than SMs (each of up to 2 * 128 / G tokens)
+        tpb = 2 * (128 // (H // H_kv))
+        blocks = min(B * -(-chunk // tpb), rows // tpb + B) * H_kv
+        many = rows * H * (d + 1) * 4 * min(64, 148 // blocks) if 2 * blocks <= 148 else 0
+        assert n - many <= max((1 << 30) + 4096, 296 // (B * H_kv) * one + 4096), (max_len, n)

@@ -127,13 +127,15 @@ def test_empty_partials_are_not_used(prefix):
 
 
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (HF, 64)])
-def test_one_long_row_in_a_wide_batch_beside_a_prompt(dtype, d):
-    """The long row's keys are cut, the prompt's rows are written directly."""
-    c = Case([(1, 50 + i) for i in range(98)] + [(1, 9000), (300, 400)], H=8, H_kv=1, d=d, page=64, dtype=dtype, W=1 << 20)
+@pytest.mark.parametrize("chunk", [300, 1300])
+def test_one_long_row_in_a_wide_batch_beside_a_prompt(dtype, d, chunk):
+    """The long row's keys are cut, the prompt's rows are written directly.  Partials are held by the rows of the call
+    (399, fewer than eight of each sequence) or by sequence (1,399)."""
+    c = Case([(1, 50 + i) for i in range(98)] + [(1, 9000), (chunk, chunk + 100)], H=8, H_kv=1, d=d, page=64, dtype=dtype, W=1 << 20)
     w = World(c)
     args = w.args()
     ws = w.kv.workspace(args)
-    assert ws.numel() >= 4 * 100 * 8 * 8 * (d + 1) * 4, "four splits of eight rows of each sequence"
+    assert ws.numel() >= 4 * min(w.rows, 100 * 8) * 8 * (d + 1) * 4, "four splits"
     w.attend(args, ws)
     assert csa.csa_sync_status() == csa.CSA_OK
     w.check()
